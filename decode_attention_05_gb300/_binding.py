@@ -18,6 +18,9 @@ FD_MERGE_KERNEL, FD_MERGE_IN_KERNEL = 0, 1
 FD_SCHEDULE_AUTO, FD_SCHEDULE_GRID, FD_SCHEDULE_PERSISTENT, FD_SCHEDULE_HEAD_GROUPS = 0, 1, 2, 3
 FD_SCHEDULE_TAIL_SHARING = 4
 FD_FROM_PROCESS = -1
+FD_ROPE_HALF, FD_ROPE_INTERLEAVED = 0, 1
+FD_DEVFLAG_SEQ_LEN, FD_DEVFLAG_PAGE, FD_DEVFLAG_TIMEOUT = 1, 2, 4
+FD_DEVFLAG_POSITION, FD_DEVFLAG_OFFSETS = 8, 16
 
 _STATUS = {0: "FD_OK", 1: "FD_ERR_INVALID_ARG", 2: "FD_ERR_UNSUPPORTED",
            3: "FD_ERR_WORKSPACE_TOO_SMALL", 4: "FD_ERR_CUDA", 5: "FD_ERR_DEVICE_FLAG"}
@@ -138,6 +141,15 @@ def _declare(L):
     L.fd_plan_resize.argtypes = [vp, i32]
     L.fd_plan_destroy.restype = None
     L.fd_plan_destroy.argtypes = [vp]
+    L.fd_append_kv.restype = ctypes.c_int
+    L.fd_append_kv.argtypes = [P, P, P, vp, vp, P, i32, vp, P, P, P, vp, vp, P, i32, vp, vp]
+    L.fd_decode_shared_prefix.restype = ctypes.c_int
+    L.fd_decode_shared_prefix.argtypes = [P, P, P, vp, vp, P, P, P, vp, vp, vp, P, i32, i32, i32,
+                                          P, vp, vp, sz, vp, O]
+    L.fd_shared_prefix_workspace_size.restype = sz
+    L.fd_shared_prefix_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i64, i64, i32, i32]
+    L.fd_resolve_prefix_splits.restype = i32
+    L.fd_resolve_prefix_splits.argtypes = [i32, i32, i32, i32, i32, i64, i32]
     L.fd_set_path.restype = ctypes.c_int
     L.fd_set_path.argtypes = [i32]
     L.fd_set_merge_mode.restype = ctypes.c_int
@@ -474,6 +486,127 @@ def merge_partials(lse_part: torch.Tensor, o_part: torch.Tensor, out: Optional[t
     do = tensor_desc(out)
     _check(lib().fd_merge_partials(B, Hq, d, S, lse_part.data_ptr(), o_part.data_ptr(),
                                    ctypes.byref(do), lse_out.data_ptr(), _stream_handle(stream)))
+    return out, lse_out
+
+
+def _ints(t: Optional[torch.Tensor], name: str) -> Optional[int]:
+    """Address of a contiguous int32 tensor (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous int32 tensor" % name)
+    return t.data_ptr()
+
+
+def _floats(t: Optional[torch.Tensor], name: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous float32 tensor" % name)
+    return t.data_ptr()
+
+
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """A cos_sin table for append_kv: f32 [max_pos, rot], row r the cosines, then the sines,
+    of r * base^(-2i / rot) for i < rot / 2, the angles computed in 64 bits."""
+    freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq[None, :]
+    return torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
+
+
+def append_kv(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+              k_cache: torch.Tensor, v_cache: torch.Tensor, seq_lens: torch.Tensor,
+              cos_sin: Optional[torch.Tensor] = None, rope_style: int = FD_ROPE_HALF,
+              pos_offset: Optional[torch.Tensor] = None,
+              cu_tokens: Optional[torch.Tensor] = None,
+              block_table: Optional[torch.Tensor] = None, page_size: int = 0,
+              k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> Optional[torch.Tensor]:
+    """fd_append_kv: write new tokens' k and v into the caches (in place), rotating q and k
+    by their positions; returns the rotated q (q_out, allocated if missing; None without q).
+    ``seq_lens`` are the lengths after the append.  Device-side input errors are reported
+    only through ``workspace`` (see ``read_device_error``)."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    B = (k_cache if block_table is None else block_table).shape[0]
+    if seq_lens.numel() != B or (pos_offset is not None and pos_offset.numel() != B):
+        raise ValueError("seq_lens and pos_offset need one entry per batch row")
+    if cu_tokens is not None and cu_tokens.numel() != B + 1:
+        raise ValueError("cu_tokens needs B + 1 entries")
+    for s in (k_scale, v_scale):
+        if s is not None and s.numel() != k_cache.shape[1]:
+            raise ValueError("scales need one entry per kv head")
+    dq, dk, dv, do = tensor_desc(q), tensor_desc(k), tensor_desc(v), tensor_desc(q_out)
+    dkc, dvc, dcs, dbt = (tensor_desc(k_cache), tensor_desc(v_cache), tensor_desc(cos_sin),
+                          tensor_desc(block_table))
+    _check(lib().fd_append_kv(
+        _ref(dq), _ref(dk), _ref(dv), _ints(cu_tokens, "cu_tokens"), _ints(seq_lens, "seq_lens"),
+        _ref(dcs), rope_style, _ints(pos_offset, "pos_offset"), _ref(do), _ref(dkc), _ref(dvc),
+        _floats(k_scale, "k_scale"), _floats(v_scale, "v_scale"), _ref(dbt), page_size,
+        None if workspace is None else workspace.data_ptr(), _stream_handle(stream)))
+    return q_out
+
+
+def shared_prefix_workspace_size(B: int, Q: int, Hq: int, Hkv: int, d: int, P: int,
+                                 L_prefix_cap: int, L_cap: int, prefix_splits: int = 0,
+                                 num_splits: int = 0) -> int:
+    return int(lib().fd_shared_prefix_workspace_size(B, Q, Hq, Hkv, d, P, L_prefix_cap, L_cap,
+                                                     prefix_splits, num_splits))
+
+
+def resolve_prefix_splits(B: int, Q: int, Hq: int, Hkv: int, P: int, L_cap: int,
+                          prefix_splits: int = 0) -> int:
+    return int(lib().fd_resolve_prefix_splits(B, Q, Hq, Hkv, P, L_cap, prefix_splits))
+
+
+def decode_attention_shared_prefix(
+        q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor,
+        prefix_lens: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+        seq_lens: torch.Tensor, group_start: Optional[torch.Tensor] = None,
+        prefix_table: Optional[torch.Tensor] = None,
+        block_table: Optional[torch.Tensor] = None, page_size: int = 0,
+        k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+        prefix_splits: int = 0, num_splits: int = 0, out: Optional[torch.Tensor] = None,
+        lse_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+        out_dtype=None, stream=None, options: Optional[FdOptions] = None
+        ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """fd_decode_shared_prefix: attention over each row's group's prompt and its own cache;
+    returns (out, lse_out).  Missing buffers are allocated with torch."""
+    if q.dim() == 4:
+        B, Qn, Hq, d = q.shape
+    else:
+        (B, Hq, d), Qn = q.shape, 1
+    P = (k_prefix if prefix_table is None else prefix_table).shape[0]
+    if seq_lens.numel() != B or prefix_lens.numel() != P:
+        raise ValueError("need one length per batch row and per prefix")
+    if group_start is not None and group_start.numel() != P + 1:
+        raise ValueError("group_start needs P + 1 entries")
+    for s in (k_scale, v_scale):
+        if s is not None and s.numel() != k_cache.shape[1]:
+            raise ValueError("scales need one entry per kv head")
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    if lse_out is None:
+        lse_out = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    elif lse_out.dtype != torch.float32 or not lse_out.is_contiguous() or lse_out.shape != q.shape[:-1]:
+        raise TypeError("lse_out must be contiguous float32 of q's shape without the last dim")
+    if workspace is None:
+        workspace = torch.zeros(shared_prefix_workspace_size(
+            B, Qn, Hq, k_cache.shape[1], d, P, _cap(k_prefix, prefix_table, page_size),
+            _cap(k_cache, block_table, page_size), prefix_splits, num_splits),
+            dtype=torch.uint8, device=q.device)
+    dq, dkp, dvp, dpt = (tensor_desc(q), tensor_desc(k_prefix), tensor_desc(v_prefix),
+                         tensor_desc(prefix_table))
+    dk, dv, dbt, do = (tensor_desc(k_cache), tensor_desc(v_cache), tensor_desc(block_table),
+                       tensor_desc(out))
+    _check(lib().fd_decode_shared_prefix(
+        _ref(dq), _ref(dkp), _ref(dvp), _ints(prefix_lens, "prefix_lens"),
+        _ints(group_start, "group_start"), _ref(dpt), _ref(dk), _ref(dv),
+        _floats(k_scale, "k_scale"), _floats(v_scale, "v_scale"), _ints(seq_lens, "seq_lens"),
+        _ref(dbt), page_size, prefix_splits, num_splits, _ref(do), lse_out.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_handle(stream), _ref(options)))
     return out, lse_out
 
 

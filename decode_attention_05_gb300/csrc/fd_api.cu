@@ -265,7 +265,8 @@ struct MapKey {
   int32_t dtype;
   uint64_t dims[5];
   uint64_t strides[4];
-  uint32_t box_rows, box_heads;
+  uint32_t box_rows, box_lines, box_heads;
+  uint32_t pad;               // no indeterminate bytes: keys are compared as memory
   bool operator==(const MapKey& o) const { return memcmp(this, &o, sizeof *this) == 0; }
 };
 
@@ -280,7 +281,7 @@ MapCache& map_cache() {
 }
 
 fd_status make_kv_map(const fd_tensor* t, uint32_t box_rows, uint32_t box_heads,
-                      CUtensorMap* out) {
+                      CUtensorMap* out, uint32_t box_lines = 0) {
   const int es = esize(t->dtype);
   const int d = (int)t->shape[3];
   MapKey key;
@@ -297,6 +298,7 @@ fd_status make_kv_map(const fd_tensor* t, uint32_t box_rows, uint32_t box_heads,
   key.strides[2] = (uint64_t)t->stride[1] * es;
   key.strides[3] = (uint64_t)t->stride[0] * es;
   key.box_rows = box_rows;
+  key.box_lines = box_lines ? box_lines : (uint32_t)key.dims[2];   // 0: whole rows
   key.box_heads = box_heads;
   MapCache& c = map_cache();
   {
@@ -310,11 +312,11 @@ fd_status make_kv_map(const fd_tensor* t, uint32_t box_rows, uint32_t box_heads,
   }
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(FD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  // One box = `box_rows` token rows, all lines, of `box_heads` consecutive kv heads: it
+  // One box = `box_rows` token rows, all lines (or `box_lines` of them), of `box_heads` consecutive kv heads: it
   // lands as [head][line][row][128 B], so the lines of one column slice of consecutive
   // rows are consecutive 128-byte lines.
-  const cuuint32_t box[5] = {(cuuint32_t)key.dims[0], box_rows, (cuuint32_t)key.dims[2],
-                             box_heads, 1};
+  const cuuint32_t box[5] = {(cuuint32_t)key.dims[0], box_rows, key.box_lines, box_heads,
+                             1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   CUtensorMap m;
   const CUtensorMapDataType ty = t->dtype == FD_BF16     ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -360,6 +362,17 @@ int32_t heuristic_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t 
 namespace fd {
 // Lets other translation units of the library report a failure through fd_last_error.
 fd_status record_error(fd_status st, const char* message) { return fail(st, "%s", message); }
+
+fd_status kv_map(const fd_tensor* t, uint32_t box_rows, uint32_t box_lines, CUtensorMap* out) {
+  return make_kv_map(t, box_rows, 1, out, box_lines);
+}
+
+bool call_path(const fd_options* options, int* path) {
+  Settings cfg;
+  if (!resolve_settings(options, &cfg)) return false;
+  *path = cfg.path;
+  return true;
+}
 
 // SM count of the current device, queried once per device (0 if it cannot be read).
 int sm_count() {

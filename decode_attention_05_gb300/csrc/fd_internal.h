@@ -138,6 +138,14 @@ cudaError_t launch_partial_kernel(Kernel kernel, dim3 grid, int threads, size_t 
 // Record `message` as the calling thread's fd_last_error() and return `st`.
 fd_status record_error(fd_status st, const char* message);
 
+// Tensor map of a cache (see make_kv_map in fd_api.cu) whose box is box_rows tokens of
+// box_lines 128-byte lines (0: whole rows) of one kv head.
+fd_status kv_map(const fd_tensor* t, uint32_t box_rows, uint32_t box_lines, CUtensorMap* out);
+
+// The kernel path a call with these options runs under (NULL: the process-wide setting);
+// false for unknown values in the options.
+bool call_path(const fd_options* options, int* path);
+
 // SM count of the current device, queried once per device (0 if it cannot be read).
 int sm_count();
 

@@ -314,6 +314,8 @@ FD_API fd_status fd_selftest_bounded_wait(void* workspace, uint32_t limit_us, vo
 #define FD_DEVFLAG_SEQ_LEN 1u   /* a seq_lens entry was outside [0, L_cap] (clamped)  */
 #define FD_DEVFLAG_PAGE 2u      /* a used block-table entry was outside [0, num_pages) */
 #define FD_DEVFLAG_TIMEOUT 4u   /* a bounded in-kernel wait gave up; that split is empty */
+#define FD_DEVFLAG_POSITION 8u  /* a token's rotary position was outside [0, max_pos)     */
+#define FD_DEVFLAG_OFFSETS 16u  /* cu_tokens or group_start is out of order or range      */
 
 /*
  * Synchronise `stream`, read the workspace's device error flags into *flags (may be
@@ -461,6 +463,111 @@ FD_API fd_status fd_decode_attention_ex(const fd_tensor* q, const fd_tensor* k_c
                                         int32_t num_splits, fd_tensor* out, float* lse_out,
                                         void* workspace, size_t workspace_bytes, void* stream,
                                         const fd_options* options);
+
+/*
+ * fd_append_kv -- write the keys and values of new tokens into a KV cache that the decode
+ * entry points read, rotating keys (and queries) by their positions on the way.
+ *
+ * Row b of the batch gets n_b new tokens and holds seq_lens[b] = L_b tokens after the call
+ * (the lengths to pass to fd_decode_attention next): its token i (0-based) goes to position
+ * p = L_b - n_b + i.  With rot columns in cos_sin, the first rot dims of each q and k head
+ * are rotated by position r = p + pos_offset[b]: for every pair (x_a, x_b),
+ *     (x_a c - x_b s,  x_b c + x_a s)   with c = cos_sin[r][i], s = cos_sin[r][rot/2 + i]
+ * in f32, rounded once to the destination's type; other dims and v are stored as they are.
+ * The angles are the caller's: for instance theta_i(r) = r * base^(-2i / rot).  (A table
+ * instead of trigonometry in the kernel: [AI-Infra], appendix on the RoPE cos/sin cache.)
+ *
+ *   q            device [T, Hq, d] or [B, Q, Hq, d], or NULL (then q_out too).
+ *   k, v         device [T, Hkv, d] or [B, Q, Hkv, d], bf16 or f32; strides as any fd_tensor's
+ *                (views of one fused projection output are fine), non-negative.
+ *   cu_tokens    NULL: one token per row (3-D, T = B) or Q per row (4-D).  Else (3-D only)
+ *                device int32 [B + 1], non-decreasing from 0: row b's tokens are
+ *                cu_tokens[b] .. cu_tokens[b + 1] - 1; tokens at or past cu_tokens[B] are
+ *                padding.  Offsets out of order are flagged (FD_DEVFLAG_OFFSETS) and their
+ *                tokens skipped.
+ *   seq_lens     device int32 [B], lengths after the append.  A row outside [0, L_cap] is
+ *                flagged (FD_DEVFLAG_SEQ_LEN) and skipped.  Tokens at negative positions
+ *                (L_b < n_b; a padded row has L_b = 0) are skipped.
+ *   cos_sin      device f32 [max_pos, rot], or NULL for no rotation; rot a multiple of 16,
+ *                at most d; rows 16-byte aligned.  A position outside [0, max_pos) is flagged
+ *                (FD_DEVFLAG_POSITION) and its token skipped.
+ *   rope_style   fd_rope_style: which dims form pair i.
+ *   pos_offset   NULL, or device int32 [B]: the rotary position of slot 0 of row b (for a
+ *                row whose cache continues a shared prompt: the prompt's length).
+ *   q_out        device, q's shape and dtype; may be q itself (same data and strides).
+ *   k_cache, v_cache, block_table, page_size  as fd_decode_attention.  Caches have k's dtype,
+ *                or FP8 E4M3 (bf16 k and v, d = 128): the code of x is the E4M3 rounding of
+ *                x / scale, at most 448 in magnitude.  A page id outside [0, num_pages) is
+ *                flagged (FD_DEVFLAG_PAGE) and its token skipped.
+ *   k_scale, v_scale  FP8 caches: device f32 [Hkv] or NULL for 1.0; NULL otherwise.
+ *   workspace    NULL, or a workspace whose header takes the flags (256 bytes suffice).
+ * A skipped token leaves q_out's rows and every cache slot as they were.  Two tokens of one
+ * call must not share a slot.  d in {64, 128}.  Errors as fd_decode_attention.
+ */
+typedef enum {
+  FD_ROPE_HALF = 0,         /* pair i = dims (i, i + rot / 2) */
+  FD_ROPE_INTERLEAVED = 1   /* pair i = dims (2 i, 2 i + 1)   */
+} fd_rope_style;
+FD_API fd_status fd_append_kv(const fd_tensor* q, const fd_tensor* k, const fd_tensor* v,
+                              const int32_t* cu_tokens, const int32_t* seq_lens,
+                              const fd_tensor* cos_sin, int32_t rope_style,
+                              const int32_t* pos_offset, fd_tensor* q_out, fd_tensor* k_cache,
+                              fd_tensor* v_cache, const float* k_scale, const float* v_scale,
+                              const fd_tensor* block_table, int32_t page_size, void* workspace,
+                              void* stream);
+
+/*
+ * fd_decode_shared_prefix -- one decode step of a batch whose rows share prompts: the keys
+ * of row b are those of its group's prompt, then its own cache's.  The softmax runs over
+ * both; each prompt's K and V are read once per group instead of once per row, since the
+ * pass over a prompt is a partial of the split-KV merge like any other ([AI-Infra] 2.6
+ * "Flash-Decoding Split-K"), computed for all rows of the group together.
+ *
+ *   q, out, lse_out, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table, num_splits,
+ *   options      as fd_decode_attention_ex, for the rows' own keys (seq_lens may be 0: the
+ *                row then sees its prompt only); out required, 16-byte aligned with strides
+ *                of whole 16 bytes.  The merge is always a kernel of its own.
+ *   k_prefix, v_prefix  the prompts, dtype of the caches: contiguous [P, Hkv, Lp_cap, d]
+ *                (prefix_table NULL) or pages [num_pages, Hkv, page_size, d].
+ *   prefix_lens  device int32 [P], 0 <= length <= Lp_cap (else clamped and flagged,
+ *                FD_DEVFLAG_SEQ_LEN).
+ *   group_start  device int32 [P + 1], non-decreasing from 0: rows group_start[p] ..
+ *                group_start[p + 1] - 1 have prompt p, rows at or past group_start[P] none.
+ *                NULL: P = 1 and all rows share it.  Entries out of order or range are
+ *                clamped and flagged (FD_DEVFLAG_OFFSETS); rows such entries leave out get
+ *                unspecified results.
+ *   prefix_table NULL, or device int32 [P, max_pages], Lp_cap = max_pages * page_size, as
+ *                block_table.
+ *   page_size    of whichever of prefix_table and block_table is given; 0 if neither is.
+ *   prefix_splits  splits of each prompt (even shares of its own length); 0: the count
+ *                fd_resolve_prefix_splits reports.
+ *   workspace    fd_shared_prefix_workspace_size bytes, otherwise as fd_decode_attention.
+ * With Q query tokens per row every one of them sees the whole prompt, and query j the own
+ * keys t <= L_b - Q + j.  A row without any key gets out = 0, lse_out = -infinity.
+ * Errors as fd_decode_attention_ex; on error nothing is launched.
+ */
+FD_API fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
+                                         const fd_tensor* v_prefix, const int32_t* prefix_lens,
+                                         const int32_t* group_start,
+                                         const fd_tensor* prefix_table, const fd_tensor* k_cache,
+                                         const fd_tensor* v_cache, const float* k_scale,
+                                         const float* v_scale, const int32_t* seq_lens,
+                                         const fd_tensor* block_table, int32_t page_size,
+                                         int32_t prefix_splits, int32_t num_splits,
+                                         fd_tensor* out, float* lse_out, void* workspace,
+                                         size_t workspace_bytes, void* stream,
+                                         const fd_options* options);
+/* Bytes of workspace such a call needs (0 for invalid sizes): P prompts of capacity
+ * L_prefix_cap, own caches of capacity L_cap.  Depends on the current device's SM count
+ * where a split count is 0. */
+FD_API size_t fd_shared_prefix_workspace_size(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv,
+                                              int32_t d, int32_t P, int64_t L_prefix_cap,
+                                              int64_t L_cap, int32_t prefix_splits,
+                                              int32_t num_splits);
+/* Split count of the prompts that such a call uses: prefix_splits, or for 0 the count that
+ * gives one wave of CTAs over (row tile, kv head, split), no split below 256 tokens. */
+FD_API int32_t fd_resolve_prefix_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t P,
+                                        int64_t L_cap, int32_t prefix_splits);
 
 /*
  * Options that fd_plan_decode uses for this plan's later decodes (copied; NULL = the
