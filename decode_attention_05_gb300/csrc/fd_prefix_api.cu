@@ -164,6 +164,9 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   // ---- splits and workspace
   const int64_t G = Hq / Hkv;
   if (Q * G > fd::kMaxRows) return unsupported("more than 64 query rows per kv head (Q x Hq / Hkv)");
+  if (G > 64 || (G & (G - 1)) != 0) return unsupported("group size not in {1, 2, 4, 8, 16, 32, 64}");
+  if ((block_table ? block_table->shape[0] : k_cache->shape[0]) != B)
+    return bad("k_cache or block_table has another batch size than q");
   const int64_t L_cap = block_table ? block_table->shape[1] * page_size : k_cache->shape[2];
   const int32_t Sp = fd_resolve_prefix_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv,
                                               (int32_t)P, Lp, prefix_splits);
@@ -200,6 +203,17 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   p.k_scale = fp8 ? k_scale : nullptr;
   p.v_scale = fp8 ? v_scale : nullptr;
 
+  // ---- the prompt pass: tensor cores for bf16, CUDA cores for f32 or when asked for
+  const bool tc = kd == FD_BF16 && path != FD_PATH_SIMT;
+  CUtensorMap tk, tv;
+  if (tc) {
+    uint32_t tokens, lines;
+    fd::prefix_tc_box(p.page_size, &tokens, &lines);
+    fd_status st = fd::kv_map(k_prefix, tokens, lines, &tk);
+    if (st == FD_OK) st = fd::kv_map(v_prefix, tokens, lines, &tv);
+    if (st != FD_OK) return st;
+  }
+
   // The rows' own keys first: this call checks their arguments and launches nothing if one
   // is wrong.
   const fd_status st = fd_decode_attention_ex(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
@@ -207,7 +221,8 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
                                               wl.own, stream, options);
   if (st != FD_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = fd::launch_prefix_simt(p, kd, (int)d, s);
+  cudaError_t e = tc ? fd::launch_prefix_tc(p, (int)d, tk, tv, s)
+                     : fd::launch_prefix_simt(p, kd, (int)d, s);
   if (e != cudaSuccess) return fd::record_error(FD_ERR_CUDA, cudaGetErrorString(e));
 
   fd::MergeParams mp;
