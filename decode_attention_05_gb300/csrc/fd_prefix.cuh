@@ -144,10 +144,10 @@ inline int64_t prefix_row_tiles(int64_t B, int64_t per_row, int64_t groups, int6
 }
 
 cudaError_t launch_prefix_simt(const PrefixParams& p, int32_t dtype, int d, cudaStream_t stream);
-// The tensor-core pass: bf16; boxes of the tensor maps tk, tv as prefix_tc_box says.
+// The tensor-core pass: bf16 or FP8 caches; boxes of the tensor maps tk, tv as prefix_tc_box says.
 void prefix_tc_box(int page_size, uint32_t* tokens, uint32_t* lines);
-cudaError_t launch_prefix_tc(const PrefixParams& p, int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                             cudaStream_t stream);
+cudaError_t launch_prefix_tc(const PrefixParams& p, bool fp8, int d, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const MergeParams& p, cudaStream_t stream);
 
 // Launch with programmatic dependent launch, as the partial kernels are.

@@ -203,8 +203,9 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   p.k_scale = fp8 ? k_scale : nullptr;
   p.v_scale = fp8 ? v_scale : nullptr;
 
-  // ---- the prompt pass: tensor cores for bf16, CUDA cores for f32 or when asked for
-  const bool tc = kd == FD_BF16 && path != FD_PATH_SIMT;
+  // ---- the prompt pass: tensor cores for bf16 and FP8, CUDA cores for f32 or when asked for
+  // (with FP8 that is refused with the rows' own keys below)
+  const bool tc = kd != FD_F32 && path != FD_PATH_SIMT;
   CUtensorMap tk, tv;
   if (tc) {
     uint32_t tokens, lines;
@@ -221,7 +222,7 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
                                               wl.own, stream, options);
   if (st != FD_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = tc ? fd::launch_prefix_tc(p, (int)d, tk, tv, s)
+  cudaError_t e = tc ? fd::launch_prefix_tc(p, fp8, (int)d, tk, tv, s)
                      : fd::launch_prefix_simt(p, kd, (int)d, s);
   if (e != cudaSuccess) return fd::record_error(FD_ERR_CUDA, cudaGetErrorString(e));
 

@@ -8,7 +8,6 @@
 // and tokens 2 tx, 2 tx + 1, and the outputs of the same rows and D / 16 dims, so a row's 16
 // threads lie in one half warp and reduce with shuffles.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "fd_prefix.cuh"
 
@@ -32,12 +31,8 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* a, float* x) {
   x[0] = bf16lo_to_f32(r.x), x[1] = bf16hi_to_f32(r.x);
   x[2] = bf16lo_to_f32(r.y), x[3] = bf16hi_to_f32(r.y);
 }
-__device__ __forceinline__ void load4(const __nv_fp8_e4m3* a, float* x) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = (float)a[i];
-}
 
-template <class TQ, class TKV, int D>
+template <class T, int D>
 __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_constant__ PrefixParams p) {
   extern __shared__ __align__(16) float smem[];
   float* qs = smem;                 // [D][kQs], rows of the tile along the last index
@@ -65,14 +60,12 @@ __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_c
     if (tid < t.rows) p.lse_part[prefix_flat_row(p, t, g, tid) * p.S + split] = kNegInf;
     return;
   }
-  const float kscale = p.k_scale != nullptr ? p.k_scale[g] : 1.f;
-  const float vscale = p.v_scale != nullptr ? p.v_scale[g] : 1.f;
   for (int i = tid; i < kBM * (D / 4); i += kThreads) {
     const int r = i % kBM, c = i / kBM;
     float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < t.rows) load4(static_cast<const TQ*>(p.q) + prefix_q_offset(p, t, g, r) + c * 4, x);
+    if (r < t.rows) load4(static_cast<const T*>(p.q) + prefix_q_offset(p, t, g, r) + c * 4, x);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) qs[(c * 4 + e) * kQs + r] = x[e] * p.scale_log2 * kscale;
+    for (int e = 0; e < 4; ++e) qs[(c * 4 + e) * kQs + r] = x[e] * p.scale_log2;
   }
 
   constexpr int DV = D / 16;
@@ -102,8 +95,8 @@ __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_c
         }
       }
       if (live) {
-        load4(static_cast<const TKV*>(p.k) + place * p.k_sb + g * p.k_sh + slot * p.k_st + c * 4, kx);
-        load4(static_cast<const TKV*>(p.v) + place * p.v_sb + g * p.v_sh + slot * p.v_st + c * 4, vx);
+        load4(static_cast<const T*>(p.k) + place * p.k_sb + g * p.k_sh + slot * p.k_st + c * 4, kx);
+        load4(static_cast<const T*>(p.v) + place * p.v_sb + g * p.v_sh + slot * p.v_st + c * 4, vx);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) ks[(c * 4 + e) * kKs + r] = kx[e];
@@ -172,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_c
     if (r >= t.rows) continue;
     const int64_t at = prefix_flat_row(p, t, g, r) * p.S + split;
     if (tx == 0) p.lse_part[at] = l[i] == 0.f ? kNegInf : (m[i] + __log2f(l[i])) * 0.6931471805599453f;
-    const float f = vscale / l[i];
+    const float f = 1.f / l[i];
 #pragma unroll
     for (int e = 0; e < DV; e += 4)
       *reinterpret_cast<float4*>(p.o_part + at * D + tx * 4 + (e / 4) * 64) =
@@ -180,9 +173,9 @@ __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_c
   }
 }
 
-template <class TQ, class TKV, int D>
+template <class T, int D>
 cudaError_t launch(const PrefixParams& p, cudaStream_t stream) {
-  auto kernel = fd_prefix_simt_kernel<TQ, TKV, D>;
+  auto kernel = fd_prefix_simt_kernel<T, D>;
   static SmemOptIn opt_in;
   cudaError_t e = opt_in.apply(kernel, (int)smem_bytes<D>());
   if (e != cudaSuccess) return e;
@@ -193,12 +186,11 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// dtype: the cache's; q is bf16 for an FP8 cache and of the cache's type otherwise.
+// dtype: that of q and the caches, f32 or bf16.
 cudaError_t launch_prefix_simt(const PrefixParams& p, int32_t dtype, int d, cudaStream_t stream) {
-  if (dtype == FD_F32) return d == 128 ? launch<float, float, 128>(p, stream) : launch<float, float, 64>(p, stream);
-  if (dtype == FD_F8E4M3) return launch<__nv_bfloat16, __nv_fp8_e4m3, 128>(p, stream);
-  return d == 128 ? launch<__nv_bfloat16, __nv_bfloat16, 128>(p, stream)
-                  : launch<__nv_bfloat16, __nv_bfloat16, 64>(p, stream);
+  if (dtype == FD_F32) return d == 128 ? launch<float, 128>(p, stream) : launch<float, 64>(p, stream);
+  return d == 128 ? launch<__nv_bfloat16, 128>(p, stream)
+                  : launch<__nv_bfloat16, 64>(p, stream);
 }
 
 }  // namespace fd

@@ -1,5 +1,6 @@
 // fd_prefix_tc.cu -- attention of many query rows over a shared prompt on the 5th-generation
-// tensor cores (fd_prefix.cuh says what the pass computes): bf16 q and caches, d 64 or 128.
+// tensor cores (fd_prefix.cuh says what the pass computes): bf16 q; bf16 caches with d 64 or
+// 128, or FP8 E4M3 caches with d = 128.
 //
 // A CTA serves one kv head, one split of one prompt and up to 256 query rows of its group, as
 // two streams of 128 rows, one per softmax warpgroup:
@@ -29,28 +30,48 @@
 // memory: Q (2 x 128 rows), then a ring of K and V tiles (32 KB at d = 128, 5 of them), each
 // [64-dim slab][token][128 B], 128-byte swizzle.  A page of fewer than 128 tokens is loaded
 // slab by slab, so that a tile has the same layout whatever the page size.
+//
+// FP8 caches: TMA fills a ring of code tiles (16 KB), and a fourth warpgroup widens them to
+// f16 (exactly: E4M3 fits f16) into the operand ring, so the products are those of f16 q, K, P
+// and V.  (8-bit products would need q and P in 8 bits.)  A kv head's scale of K multiplies
+// the scores, its scale of V the output.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include "fd_prefix.cuh"
 #include "fd_tcgen05.cuh"
 
 namespace fd {
 namespace {
 
-constexpr int kRows = 128, kTok = 128, kThreads = 384;
+constexpr int kRows = 128, kTok = 128;
 constexpr uint32_t kCols = 512, kOCol = 256;
 constexpr int kMaxStages = 8;
 
-template <int D>
+template <int D_, bool FP8_>
 struct Shape {
+  static constexpr int D = D_;
+  static constexpr bool FP8 = FP8_;
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr uint32_t TYPE = FP8 ? 0u : 1u;               // operands f16 or bf16
   static constexpr int SLABS = D / 64;
   static constexpr uint32_t SLAB_BYTES = kTok * 128;            // 64 dims of 128 tokens
   static constexpr uint32_t TILE_BYTES = SLABS * SLAB_BYTES;
-  static constexpr int STAGES = D == 128 ? 5 : 8;
+  static constexpr int STAGES = FP8 ? 4 : D == 128 ? 5 : 8;
   static constexpr uint32_t RING_OFF = 2 * TILE_BYTES;          // behind Q
-  static constexpr uint32_t CTL_OFF = RING_OFF + STAGES * TILE_BYTES;
+  // FP8: tiles of codes.  Two, and two more in the second row tile's place of Q where there
+  // is none (with few rows the pass is bound by how much it has in flight).
+  static constexpr uint32_t RAW_BYTES = kTok * 128;
+  static constexpr uint32_t RAW_OFF = RING_OFF + STAGES * TILE_BYTES;
+  static constexpr uint32_t CTL_OFF = RAW_OFF + (FP8 ? 2 * RAW_BYTES : 0);
+  static __device__ __forceinline__ uint32_t raw_offset(int st) {
+    return st < 2 ? RAW_OFF + st * RAW_BYTES : TILE_BYTES + (st - 2) * RAW_BYTES;
+  }
 };
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];   // ring: a K or V tile has landed / been read
+  uint64_t raw_full[4], raw_empty[4];             // FP8: a tile of codes has landed / been widened
   uint64_t s_full[2];                             // S of the stream's next tile is complete
   uint64_t p_half[2][2];                          // the first / second 64 tokens of P are in place
   uint64_t o_full[2];                             // the stream's last product is complete
@@ -61,11 +82,13 @@ struct Ctl {
   PrefixTile tile;
 };
 
-template <int D>
+template <class SH>
 constexpr size_t smem_bytes() {
-  return 1024 + Shape<D>::CTL_OFF + sizeof(Ctl);
+  return 1024 + SH::CTL_OFF + sizeof(Ctl);
 }
-static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024, "one CTA per SM");
+static_assert(smem_bytes<Shape<128, false>>() <= 227 * 1024 && smem_bytes<Shape<64, false>>() <= 227 * 1024 &&
+                  smem_bytes<Shape<128, true>>() <= 227 * 1024,
+              "one CTA per SM");
 
 __device__ __forceinline__ bool aborted(Ctl* c) {
   return *reinterpret_cast<volatile int32_t*>(&c->abort) != 0;
@@ -118,6 +141,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 __device__ __forceinline__ void store8(float* a, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "f"(v[0]),
                "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
@@ -125,18 +152,20 @@ __device__ __forceinline__ void store8(float* a, const float* v) {
 }
 
 // ---------------------------------------------------------------- TMA producer (one warp)
-// Ring entry 2 n is the K tile n of the split, 2 n + 1 its V tile.
-template <int D>
-__device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n_tiles,
-                        const CUtensorMap* tk, const CUtensorMap* tv, uint32_t ring, Ctl* ctl,
-                        int lane) {
-  using SH = Shape<D>;
+// Ring entry 2 n is the K tile n of the split, 2 n + 1 its V tile.  bf16 tiles go to the
+// operand ring, codes to the raw one.
+template <class SH>
+__device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n_tiles, int raw_stages,
+                        const CUtensorMap* tk, const CUtensorMap* tv, uint32_t base, Ctl* ctl, int lane) {
   const uint64_t pol = policy_evict_first();
   const bool paged = p.table != nullptr;
   const int ps = p.page_size;
   const int boxes = paged && ps < kTok ? kTok / ps : 1;      // pages of a tile
   const int64_t used = paged ? (t.L + ps - 1) >> p.log2_page : 0;
-  int issued = 0;
+  const int stages = SH::FP8 ? raw_stages : SH::STAGES;
+  uint64_t* fulls = SH::FP8 ? ctl->raw_full : ctl->full;
+  uint64_t* empties = SH::FP8 ? ctl->raw_empty : ctl->empty;
+  int issued = 0, st = 0, round = 0;          // entry, its stage, and how often the ring wrapped
   bool ok = true;
   for (int n = 0; n < n_tiles && ok; ++n) {
     const int64_t t0 = t.lo + (int64_t)n * kTok;
@@ -157,38 +186,86 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
     }
     __syncwarp();
     for (int kv = 0; kv < 2; ++kv) {
-      const int st = issued % SH::STAGES;
-      const uint32_t full = smem_addr(&ctl->full[st]);
-      if (issued >= SH::STAGES)
-        ok = warp_wait(ctl, smem_addr(&ctl->empty[st]), ((issued / SH::STAGES) - 1) & 1);
+      const uint32_t full = smem_addr(&fulls[st]);
+      if (round > 0) ok = warp_wait(ctl, smem_addr(&empties[st]), (round - 1) & 1);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(full, SH::TILE_BYTES);
+      if (lane == 0) mbar_arrive_expect_tx(full, SH::FP8 ? SH::RAW_BYTES : SH::TILE_BYTES);
       __syncwarp();
-      const uint32_t dst = ring + st * SH::TILE_BYTES;
+      const uint32_t dst = base + (SH::FP8 ? SH::raw_offset(st) : SH::RING_OFF + st * SH::TILE_BYTES);
       const CUtensorMap* map = kv ? tv : tk;
       if (boxes == 1) {
         if (lane == 0) tma_load_5d(dst, map, full, 0, slot, 0, g, id, pol);
       } else if (lane < boxes) {
 #pragma unroll
-        for (int s = 0; s < SH::SLABS; ++s)
-          tma_load_5d(dst + s * SH::SLAB_BYTES + lane * ps * 128, map, full, 0, 0, s, g, id, pol);
+        for (int x = 0; x < (SH::FP8 ? 1 : SH::SLABS); ++x)
+          tma_load_5d(dst + x * SH::SLAB_BYTES + lane * ps * 128, map, full, 0, 0, x, g, id, pol);
       }
       ++issued;
+      if (++st == stages) st = 0, ++round;
     }
   }
   if (!ok) {                        // let the copies in flight land before the CTA ends
     if (lane == 0) set_abort(p, ctl);
-    for (int i = max(0, issued - SH::STAGES); i < issued; ++i)
-      mbar_wait(smem_addr(&ctl->full[i % SH::STAGES]), (i / SH::STAGES) & 1);
+    for (int i = max(0, issued - stages); i < issued; ++i)
+      mbar_wait(smem_addr(&fulls[i % stages]), (i / stages) & 1);
   }
 }
 
+// ---------------------------------------------------------------- widening (FP8, a warpgroup)
+// Thread r widens token row r of every tile: 16 codes of one 16-byte group become two groups
+// of f16.  A quarter warp's eight rows hit eight different bank groups in both layouts.  Rows
+// of tokens without weight become zeros.
+template <class SH>
+__device__ void widen(const PrefixParams& p, const PrefixTile& t, int n_tiles, int raw_stages, uint8_t* base,
+                      Ctl* ctl, int r) {
+  const int lane = r & 31;
+  const bool pages = p.table != nullptr && p.page_size < kTok;
+  bool ok = true;
+  int rs = 0, round = 0;
+  for (int e = 0; e < 2 * n_tiles; ++e) {
+    const int n = e >> 1, st = e % SH::STAGES;
+    ok = warp_wait(ctl, smem_addr(&ctl->raw_full[rs]), round & 1);
+    if (ok && e >= SH::STAGES) ok = warp_wait(ctl, smem_addr(&ctl->empty[st]), ((e / SH::STAGES) - 1) & 1);
+    if (!ok) break;
+    const int64_t tok = t.lo + (int64_t)n * kTok + r;
+    const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[n & 7]);
+    const bool live = tok < t.hi && !((bad >> (pages ? r >> p.log2_page : 0)) & 1u);
+    const uint8_t* src = base + SH::raw_offset(rs) + r * 128;
+    uint8_t* dst = base + SH::RING_OFF + st * SH::TILE_BYTES + r * 128;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 x = live ? *reinterpret_cast<const uint4*>(src + ((c ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t h[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
+            : "r"(w[i]));
+      }
+      uint8_t* slab = dst + (c >> 2) * SH::SLAB_BYTES;
+      const int c0 = (2 * c) & 7;
+      *reinterpret_cast<uint4*>(slab + ((c0 ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(slab + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_addr(&ctl->raw_empty[rs]));
+      mbar_arrive(smem_addr(&ctl->full[st]));
+    }
+    if (++rs == raw_stages) rs = 0, ++round;
+  }
+  if (!ok && lane == 0) set_abort(p, ctl);
+}
+
 // ---------------------------------------------------------------- product issuer (one thread)
-template <int D>
+template <class SH>
 __device__ void issue(const PrefixParams& p, int n_tiles, bool two_rows, uint32_t qbase,
                       uint32_t ring, Ctl* ctl, uint32_t tmem) {
-  using SH = Shape<D>;
-  constexpr uint32_t id_s = instr_desc(kRows, kTok, 0), id_o = instr_desc(kRows, D, 1);
+  constexpr int D = SH::D;
+  constexpr uint32_t id_s = instr_desc(kRows, kTok, 0, SH::TYPE), id_o = instr_desc(kRows, D, 1, SH::TYPE);
   const int step = two_rows ? 1 : 2;          // a stream's next tile
   auto tile_at = [&](int e) { return ring + (uint32_t)(e % SH::STAGES) * SH::TILE_BYTES; };
   auto landed = [&](int e) {
@@ -249,11 +326,11 @@ __device__ void issue(const PrefixParams& p, int n_tiles, bool two_rows, uint32_
 
 // ---------------------------------------------------------------- softmax (a warpgroup)
 // Stream w, lane row r.  False if a wait gave up.
-template <int D>
+template <class SH>
 __device__ bool softmax(const PrefixParams& p, const PrefixTile& t, int n_tiles, bool two_rows,
                         int w, int r, float sl2, uint8_t* ring, Ctl* ctl, uint32_t tmem, float& m,
                         float& l) {
-  using SH = Shape<D>;
+  constexpr int D = SH::D;
   const int lane = r & 31;
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
   const uint32_t sc = tmem + lanes + w * kTok, oc = tmem + lanes + kOCol + w * D;
@@ -277,16 +354,18 @@ __device__ bool softmax(const PrefixParams& p, const PrefixTile& t, int n_tiles,
         const bool out = j >= live || ((bad >> (pages ? j >> log2_page : 0)) & 1u);
         s[j] = out ? kNegInf : s[j];
       }
-      // Their V rows may hold anything, and 0 * NaN would reach O: clear them.
-      const int e = 2 * n + 1;
-      if (!warp_wait(ctl, smem_addr(&ctl->full[e % SH::STAGES]), (e / SH::STAGES) & 1)) return false;
-      if (r >= live || ((bad >> (pages ? r >> log2_page : 0)) & 1u)) {
-        uint8_t* v = ring + (size_t)(e % SH::STAGES) * SH::TILE_BYTES + r * 128;
+      if constexpr (!SH::FP8) {     // (widen() has cleared them)
+        // Their V rows may hold anything, and 0 * NaN would reach O: clear them.
+        const int e = 2 * n + 1;
+        if (!warp_wait(ctl, smem_addr(&ctl->full[e % SH::STAGES]), (e / SH::STAGES) & 1)) return false;
+        if (r >= live || ((bad >> (pages ? r >> log2_page : 0)) & 1u)) {
+          uint8_t* v = ring + (size_t)(e % SH::STAGES) * SH::TILE_BYTES + r * 128;
 #pragma unroll
-        for (int c = 0; c < SH::SLABS * 8; ++c)
-          *reinterpret_cast<uint4*>(v + (c >> 3) * SH::SLAB_BYTES + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < SH::SLABS * 8; ++c)
+            *reinterpret_cast<uint4*>(v + (c >> 3) * SH::SLAB_BYTES + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
       }
-      fence_proxy_async_smem();
     }
     float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -327,7 +406,7 @@ __device__ bool softmax(const PrefixParams& p, const PrefixTile& t, int n_tiles,
         a = ex2(a);
         b = ex2(b);
         sum[j & 3] = add2(sum[j & 3], pair(a, b));
-        pk[j] = pack_bf16(a, b);
+        pk[j] = SH::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
       }
       tc_st32w(sc + half * 32, pk);
       tc_fence_before();
@@ -428,11 +507,11 @@ __device__ void merge_rows(const PrefixParams& p, const PrefixTile& t, int g, in
   if (mine && w == 0) p.lse_part[at] = lse_of(M, L);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class SH>
+__global__ void __launch_bounds__(SH::THREADS, 1)
     fd_prefix_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const __grid_constant__ PrefixParams p) {
-  using SH = Shape<D>;
+  constexpr int D = SH::D;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -442,8 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = blockIdx.x, g = blockIdx.y;
   if (tid == 0) {
     for (int s = 0; s < SH::STAGES; ++s) {
-      mbar_init(smem_addr(&ctl->full[s]), 1);
+      mbar_init(smem_addr(&ctl->full[s]), SH::FP8 ? 4 : 1);   // FP8: the widening warps arrive
       mbar_init(smem_addr(&ctl->empty[s]), 1);
+    }
+    for (int s = 0; SH::FP8 && s < 4; ++s) {
+      mbar_init(smem_addr(&ctl->raw_full[s]), 1);
+      mbar_init(smem_addr(&ctl->raw_empty[s]), 4);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_addr(&ctl->s_full[w]), 1);
@@ -479,22 +562,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PrefixTile t = ctl->tile;
   const int n_tiles = found && t.lo < t.hi ? (int)((t.hi - t.lo + kTok - 1) / kTok) : 0;
   const bool two_rows = t.rows > kRows;
+  const int raw_stages = two_rows ? 2 : 4;
 
   if (n_tiles > 0) {
-    // Registers: 216 for the softmax threads, 72 for the others; 2 x 216 + 72 is what the
-    // three warpgroups were launched with (168 each).
-    if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // Registers of the warpgroups (softmax, softmax, producer and issuer, widening): 216 +
+    // 216 + 72 is what three were launched with (168 each), 184 + 184 + 56 + 88 four (128).
+    if (warp >= 12) {
+      if constexpr (SH::FP8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        widen<SH>(p, t, n_tiles, raw_stages, base, ctl, tid & 127);
+      }
+    } else if (warp >= 8) {
+      if constexpr (SH::FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp == 8) {
-        produce<D>(p, t, g, n_tiles, &tk, &tv, smem_addr(ring), ctl, lane);
+        produce<SH>(p, t, g, n_tiles, raw_stages, &tk, &tv, smem_addr(base), ctl, lane);
       } else if (warp == 9) {
         named_bar_sync(2, 288);               // Q is in place
-        if (lane == 0) issue<D>(p, n_tiles, two_rows, smem_addr(base), smem_addr(ring), ctl, tmem);
+        if (lane == 0) issue<SH>(p, n_tiles, two_rows, smem_addr(base), smem_addr(ring), ctl, tmem);
         __syncwarp();
       }
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+      if constexpr (SH::FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       const int w = warp >> 2, r = tid & 127;
+      // A scale of K multiplies the scores (its sign q, since the running maximum is taken
+      // before the factor; a factor of 0 becomes one that only keeps -inf what it is).
+      const float ks = p.k_scale != nullptr ? p.k_scale[g] : 1.f;
+      const float vs = p.v_scale != nullptr ? p.v_scale[g] : 1.f;
+      const float sl2 = SH::FP8 ? fmaxf(p.scale_log2 * fabsf(ks), 1e-37f) : p.scale_log2;
       // Q to shared memory, [64-dim slab][row][128 B] with 16-byte groups XORed by the row.
       // Two row tiles: a thread its row; one: the two threads of a row half of it each.
       {
@@ -505,14 +601,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* dst = base + (two_rows ? w * SH::TILE_BYTES : 0u) + r * 128;
         const int c0 = two_rows ? 0 : w * (D / 16), c1 = two_rows ? D / 8 : c0 + D / 16;
 #pragma unroll 4
-        for (int c = c0; c < c1; ++c)
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * SH::SLAB_BYTES + (((c & 7) ^ (r & 7)) << 4)) =
-              live ? src[c] : make_uint4(0, 0, 0, 0);
+        for (int c = c0; c < c1; ++c) {
+          uint4 x = live ? src[c] : make_uint4(0, 0, 0, 0);
+          if constexpr (SH::FP8) {            // q as f16
+            uint32_t* y = &x.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float f = ks < 0.f ? -1.f : 1.f;
+              y[i] = pack_f16(bf16lo_to_f32(y[i]) * f, bf16hi_to_f32(y[i]) * f);
+            }
+          }
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * SH::SLAB_BYTES + (((c & 7) ^ (r & 7)) << 4)) = x;
+        }
       }
       fence_proxy_async_smem();
       named_bar_sync(2, 288);
       float m, l;
-      if (!softmax<D>(p, t, n_tiles, two_rows, w, r, p.scale_log2, ring, ctl, tmem, m, l) && lane == 0)
+      if (!softmax<SH>(p, t, n_tiles, two_rows, w, r, sl2, ring, ctl, tmem, m, l) && lane == 0)
         set_abort(p, ctl);
       named_bar_sync(1, 256);                 // both streams are done, or one gave up
       if (aborted(ctl)) {
@@ -520,9 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row < t.rows && (two_rows || w == 0))
           p.lse_part[prefix_flat_row(p, t, g, row) * p.S + split] = kNegInf;
       } else if (two_rows) {
-        write_rows<D>(p, t, g, split, w, r, m, l, 1.f, tmem);
+        write_rows<D>(p, t, g, split, w, r, m, l, vs, tmem);
       } else {
-        merge_rows<D>(p, t, g, split, n_tiles, w, r, m, l, 1.f, ring, ctl, tmem);
+        merge_rows<D>(p, t, g, split, n_tiles, w, r, m, l, vs, ring, ctl, tmem);
       }
     }
   } else if (found) {               // nothing of the prompt in this split
@@ -537,22 +642,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <class SH>
 cudaError_t launch(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  auto kernel = fd_prefix_tc_kernel<D>;
+  auto kernel = fd_prefix_tc_kernel<SH>;
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.apply(kernel, (int)smem_bytes<D>());
+  cudaError_t e = opt_in.apply(kernel, (int)smem_bytes<SH>());
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.S, (unsigned)p.Hkv,
                   (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start ? p.P : 1, 2 * kRows));
-  return launch_pdl(kernel, grid, kThreads, smem_bytes<D>(), stream, tk, tv, p);
+  return launch_pdl(kernel, grid, SH::THREADS, smem_bytes<SH>(), stream, tk, tv, p);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_tc(const PrefixParams& p, int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                             cudaStream_t stream) {
-  return d == 128 ? launch<128>(p, tk, tv, stream) : launch<64>(p, tk, tv, stream);
+cudaError_t launch_prefix_tc(const PrefixParams& p, bool fp8, int d, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t stream) {
+  if (fp8) return launch<Shape<128, true>>(p, tk, tv, stream);
+  return d == 128 ? launch<Shape<128, false>>(p, tk, tv, stream) : launch<Shape<64, false>>(p, tk, tv, stream);
 }
 
 // Tokens and 128-byte lines of this kernel's TMA boxes.
