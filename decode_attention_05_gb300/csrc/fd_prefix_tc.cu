@@ -3,7 +3,7 @@
 // 128, or FP8 E4M3 caches with d = 128.
 //
 // A CTA serves one kv head, one split of one prompt and up to 256 query rows of its group, as
-// two streams of 128 rows, one per softmax warpgroup:
+// two streams of 128 rows, one softmax warpgroup each:
 //   S_w[128 rows, 128 tokens] = Q_w . K_tile^T     tcgen05.mma, both operands in shared memory
 //   thread r of the warpgroup reads row r of S from tensor memory, keeps the running maximum m
 //   and sum l of the softmax, and writes P = bf16(2^(S - m)) over S's own columns
@@ -14,24 +14,26 @@
 // two independent partial softmaxes that are merged at the end: one stream's products run
 // while the other's softmax does, whatever the number of rows.
 //
-// One thread issues all products: P V of a stream's tile, then at once Q K^T of its next tile
-// (in order behind the read of P, whose columns it overwrites), then the other stream's.  So
-// the tensor cores work on one stream while the other's warps do their softmax.  O is rescaled
-// only when a tile's maximum exceeds m by more than 8 (base 2): weights then reach at most 2^8,
-// and l and O use the same m, so the result is the same.
+// Each stream has a warp that issues its products: P V of a tile, then at once Q K^T of the
+// next (in order behind the read of P, whose columns it overwrites).  So the tensor cores work
+// on one stream while the other's warps do their softmax.  The softmax uses the maximum m of
+// the tiles before, and O is rescaled (and the tile's weights formed again) only when the
+// tile's maximum exceeds m by more than 8 (base 2): weights then reach at most 2^8, and l and
+// O use the same m, so the result is the same -- and the exponentials need not wait for the
+// maximum.
 //
 // Bound: with 256 rows a CTA does 2 x 4 x 128 x 128 x d flops on a tile of 512 d bytes of K
 // and V: the tensor cores (2048 cycles a tile at d = 128) and the SM's share of HBM bandwidth
 // (about 24 bytes a cycle: 2700 cycles) are near balance; several row tiles read a prompt's
 // tiles from L2.
 //
-// Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 the TMA producer, 9 the issuer.  Tensor
+// Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 the TMA producer, 9 and 10 the issuers.  Tensor
 // memory: S_0, S_1 (128 columns each, P over their first halves), O_0, O_1 (d each).  Shared
 // memory: Q (2 x 128 rows), then a ring of K and V tiles (32 KB at d = 128, 5 of them), each
 // [64-dim slab][token][128 B], 128-byte swizzle.  A page of fewer than 128 tokens is loaded
 // slab by slab, so that a tile has the same layout whatever the page size.
 //
-// FP8 caches: TMA fills a ring of code tiles (16 KB), and a fourth warpgroup widens them to
+// FP8 caches: TMA fills a ring of code tiles (16 KB), and another warpgroup widens them to
 // f16 (exactly: E4M3 fits f16) into the operand ring, so the products are those of f16 q, K, P
 // and V.  (8-bit products would need q and P in 8 bits.)  A kv head's scale of K multiplies
 // the scores, its scale of V the output.
@@ -46,7 +48,7 @@ namespace {
 
 constexpr int kRows = 128, kTok = 128;
 constexpr uint32_t kCols = 512, kOCol = 256;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 9;
 
 template <int D_, bool FP8_>
 struct Shape {
@@ -59,6 +61,11 @@ struct Shape {
   static constexpr uint32_t TILE_BYTES = SLABS * SLAB_BYTES;
   static constexpr int STAGES = FP8 ? 4 : D == 128 ? 5 : 8;
   static constexpr uint32_t RING_OFF = 2 * TILE_BYTES;          // behind Q
+  // The ring of a CTA with one row tile (bf16) also has the second one's place of Q.
+  static __device__ __forceinline__ uint32_t ring_off(bool two_rows) {
+    return FP8 || two_rows ? RING_OFF : RING_OFF - TILE_BYTES;
+  }
+  static __device__ __forceinline__ int stages(bool two_rows) { return FP8 || two_rows ? STAGES : STAGES + 1; }
   // FP8: tiles of codes.  Two, and two more in the second row tile's place of Q where there
   // is none (with few rows the pass is bound by how much it has in flight).
   static constexpr uint32_t RAW_BYTES = kTok * 128;
@@ -84,7 +91,7 @@ struct Ctl {
 
 template <class SH>
 constexpr size_t smem_bytes() {
-  return 1024 + SH::CTL_OFF + sizeof(Ctl);
+  return SH::CTL_OFF + sizeof(Ctl);
 }
 static_assert(smem_bytes<Shape<128, false>>() <= 227 * 1024 && smem_bytes<Shape<64, false>>() <= 227 * 1024 &&
                   smem_bytes<Shape<128, true>>() <= 227 * 1024,
@@ -97,9 +104,12 @@ __device__ __forceinline__ void set_abort(const PrefixParams& p, Ctl* c) {
   *reinterpret_cast<volatile int32_t*>(&c->abort) = 1;
   atomicOr(p.flags, kDevFlagTimeout);
 }
-// A bounded wait that also gives up once another role has.
+// A bounded wait that also gives up once another role has.  The clock is read only after some
+// tries: a wait in a running pipeline ends within a few.
 __device__ __forceinline__ bool wait_or_abort(Ctl* c, uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (!mbar_probe(bar, parity, 200u)) {
     if (aborted(c) || global_ns() - t0 > kWaitLimitNs) return false;
@@ -108,15 +118,9 @@ __device__ __forceinline__ bool wait_or_abort(Ctl* c, uint32_t bar, uint32_t par
 }
 // The same for a warp whose lanes have to agree.
 __device__ __forceinline__ bool warp_wait(Ctl* c, uint32_t bar, uint32_t parity) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_or_abort(c, bar, parity));
 }
 
-// 128 columns of this thread's lane.
-__device__ __forceinline__ void ld128(uint32_t taddr, float* v) {
-  tc_ld32x2(taddr, taddr + 32, v);
-  tc_ld32x2(taddr + 64, taddr + 96, v + 64);
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -156,13 +160,14 @@ __device__ __forceinline__ void store8(float* a, const float* v) {
 // operand ring, codes to the raw one.
 template <class SH>
 __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n_tiles, int raw_stages,
-                        const CUtensorMap* tk, const CUtensorMap* tv, uint32_t base, Ctl* ctl, int lane) {
+                        bool two_rows, const CUtensorMap* tk, const CUtensorMap* tv, uint32_t base, Ctl* ctl,
+                        int lane) {
   const uint64_t pol = policy_evict_first();
   const bool paged = p.table != nullptr;
   const int ps = p.page_size;
   const int boxes = paged && ps < kTok ? kTok / ps : 1;      // pages of a tile
   const int64_t used = paged ? (t.L + ps - 1) >> p.log2_page : 0;
-  const int stages = SH::FP8 ? raw_stages : SH::STAGES;
+  const int stages = SH::FP8 ? raw_stages : SH::stages(two_rows);
   uint64_t* fulls = SH::FP8 ? ctl->raw_full : ctl->full;
   uint64_t* empties = SH::FP8 ? ctl->raw_empty : ctl->empty;
   int issued = 0, st = 0, round = 0;          // entry, its stage, and how often the ring wrapped
@@ -191,7 +196,7 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(full, SH::FP8 ? SH::RAW_BYTES : SH::TILE_BYTES);
       __syncwarp();
-      const uint32_t dst = base + (SH::FP8 ? SH::raw_offset(st) : SH::RING_OFF + st * SH::TILE_BYTES);
+      const uint32_t dst = base + (SH::FP8 ? SH::raw_offset(st) : SH::ring_off(two_rows) + st * SH::TILE_BYTES);
       const CUtensorMap* map = kv ? tv : tk;
       if (boxes == 1) {
         if (lane == 0) tma_load_5d(dst, map, full, 0, slot, 0, g, id, pol);
@@ -260,106 +265,150 @@ __device__ void widen(const PrefixParams& p, const PrefixTile& t, int n_tiles, i
   if (!ok && lane == 0) set_abort(p, ctl);
 }
 
-// ---------------------------------------------------------------- product issuer (one thread)
+// ---------------------------------------------------------------- product issuer (a warp a stream)
+// The whole warp walks the schedule, so that operand descriptors and addresses stay in uniform
+// registers; one elected lane issues the instructions.  (With the schedule inside a branch of
+// one lane every product took about 100 cycles to issue, more than it takes to run.)
+__device__ __forceinline__ bool elected() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 template <class SH>
-__device__ void issue(const PrefixParams& p, int n_tiles, bool two_rows, uint32_t qbase,
-                      uint32_t ring, Ctl* ctl, uint32_t tmem) {
+__device__ __forceinline__ void issue(const PrefixParams& p, int w, int n_tiles_, bool two_rows_, uint32_t base,
+                                      Ctl* ctl) {
   constexpr int D = SH::D;
   constexpr uint32_t id_s = instr_desc(kRows, kTok, 0, SH::TYPE), id_o = instr_desc(kRows, D, 1, SH::TYPE);
+  const int n_tiles = __shfl_sync(0xffffffffu, n_tiles_, 0);
+  const int two_rows = __shfl_sync(0xffffffffu, two_rows_ ? 1 : 0, 0);
   const int step = two_rows ? 1 : 2;          // a stream's next tile
-  auto tile_at = [&](int e) { return ring + (uint32_t)(e % SH::STAGES) * SH::TILE_BYTES; };
-  auto landed = [&](int e) {
-    return wait_or_abort(ctl, smem_addr(&ctl->full[e % SH::STAGES]), (e / SH::STAGES) & 1);
+  const uint64_t q = smem_desc(base + (two_rows ? w * SH::TILE_BYTES : 0u), 0, 1024);
+  const uint32_t ring = base + SH::ring_off(two_rows != 0);
+  const int stages = SH::stages(two_rows != 0);
+  const uint64_t k0 = smem_desc(ring, 0, 1024), v0 = smem_desc(ring, SH::SLAB_BYTES, 1024);
+  constexpr uint32_t kTile16 = SH::TILE_BYTES >> 4, kSlab16 = SH::SLAB_BYTES >> 4;   // descriptor units
+  // Ring position (stage, parity of its use) of the next K and V tile of this stream.
+  const int jump = 2 * step;
+  int ks = 0, kp = 0, vs = 0, vp = 0;
+  auto advance = [&](int& st, int& par, int by) {
+    st += by;
+    if (st >= stages) st -= stages, par ^= 1;
   };
-  auto release = [&](int e) { tc_commit(smem_addr(&ctl->empty[e % SH::STAGES])); };
-  auto scores = [&](int w, int n) {
-    const uint32_t q = qbase + (two_rows ? w * SH::TILE_BYTES : 0u), k = tile_at(2 * n);
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const uint32_t off = (ks >> 2) * SH::SLAB_BYTES + (ks & 3) * 32u;
-      tc_mma_ss(tmem + w * kTok, smem_desc(q + off, 0, 1024), smem_desc(k + off, 0, 1024), id_s, ks > 0);
+  if (!two_rows && w == 1) advance(ks, kp, 2);
+  vs = ks, vp = kp;
+  advance(vs, vp, 1);
+  // A ring entry is free once both issuers have committed to it: with one row tile its only
+  // user does so twice.
+  auto release = [&](int st) {
+    if (elected()) {
+      tc_commit(smem_addr(&ctl->empty[st]));
+      if (!two_rows) tc_commit(smem_addr(&ctl->empty[st]));
     }
-    tc_commit(smem_addr(&ctl->s_full[w]));
+    __syncwarp();
+  };
+  auto scores = [&]() {
+    const uint64_t k = k0 + (uint32_t)ks * kTile16;
+    if (elected()) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t off = (i >> 2) * kSlab16 + (i & 3) * 2u;
+        tc_mma_ss(w * kTok, q + off, k + off, id_s, i > 0);
+      }
+      tc_commit(smem_addr(&ctl->s_full[w]));
+    }
+    __syncwarp();
+    release(ks);
+    advance(ks, kp, jump);
   };
   bool ok = true;
-  for (int w = 0; w < 2 && ok; ++w) {         // the streams' first scores
-    const int n = two_rows ? 0 : w;
-    if (n >= n_tiles) break;
-    ok = landed(2 * n);
-    if (!ok) break;
-    scores(w, n);
-    if (!two_rows || w == 1) release(2 * n);
+  const int first = two_rows ? 0 : w;
+  if (first < n_tiles) {
+    ok = warp_wait(ctl, smem_addr(&ctl->full[ks]), kp);
+    if (ok) scores();
   }
-  for (int n = 0; n < n_tiles && ok; ++n) {
-    ok = landed(2 * n + 1);
-    const int next = n + step, i = two_rows ? n : n >> 1;
-    for (int w = two_rows ? 0 : n & 1; w < 2 && ok; ++w) {
-      const uint32_t v = tile_at(2 * n + 1);
+  int i = 0;
+  for (int n = first; n < n_tiles && ok; n += step, ++i) {
+    const bool more = n + step < n_tiles;
+    ok = warp_wait(ctl, smem_addr(&ctl->full[vs]), vp);
+    const uint64_t v = v0 + (uint32_t)vs * kTile16;
 #pragma unroll
-      for (int ks = 0; ks < kTok / 16; ++ks) {
-        if (ks % 4 == 0) {
-          ok = wait_or_abort(ctl, smem_addr(&ctl->p_half[w][ks / 4]), i & 1);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        tc_mma_ts(tmem + kOCol + w * D, tmem + w * kTok + ks * 8,
-                  smem_desc(v + ks * 2048u, SH::SLAB_BYTES, 1024), id_o, (i > 0 || ks > 0) ? 1u : 0u);
-      }
+    for (int half = 0; half < 2; ++half) {
+      ok = ok && warp_wait(ctl, smem_addr(&ctl->p_half[w][half]), i & 1);
       if (!ok) break;
-      const bool last_use = !two_rows || w == 1;
-      if (last_use) release(2 * n + 1);
-      if (next < n_tiles) {
-        if (!two_rows || w == 0) ok = landed(2 * next);
-        if (!ok) break;
-        scores(w, next);
-        if (last_use) release(2 * next);
-      } else {
-        tc_commit(smem_addr(&ctl->o_full[w]));
+      tc_fence_after();
+      if (elected()) {
+#pragma unroll
+        for (int x = half * 4; x < half * 4 + 4; ++x)
+          tc_mma_ts(kOCol + w * D, w * kTok + x * 8, v + x * (2048u >> 4), id_o, (i > 0 || x > 0) ? 1u : 0u);
+        if (half == 1 && !more) tc_commit(smem_addr(&ctl->o_full[w]));
       }
-      if (!two_rows) break;
+      __syncwarp();
     }
+    if (!ok) break;
+    if (more) {
+      ok = warp_wait(ctl, smem_addr(&ctl->full[ks]), kp);
+      if (!ok) break;
+      scores();                     // S of the next tile is complete behind P V
+    }
+    release(vs);
+    advance(vs, vp, jump);
   }
-  if (!ok) set_abort(p, ctl);
-  tc_commit(smem_addr(&ctl->mma_done));       // never leave with products in flight
+  if (!ok && elected()) set_abort(p, ctl);
+  __syncwarp();
+  if (elected()) tc_commit(smem_addr(&ctl->mma_done));   // never leave with products in flight
+  __syncwarp();
   if (!mbar_wait(smem_addr(&ctl->mma_done), 0)) atomicOr(p.flags, kDevFlagTimeout);
 }
 
-// ---------------------------------------------------------------- softmax (a warpgroup)
+// ---------------------------------------------------------------- softmax (a warpgroup a stream)
+// The weights 2^(s sl2 - base) of 64 scores as pairs of 16-bit operands, added to `sum`.
+template <class SH>
+__device__ __forceinline__ void weights(const float* s, uint64_t scale2, uint64_t off2, uint32_t* pk, uint64_t* sum) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float a, b;
+    unpair(fma2(pair(s[2 * j], s[2 * j + 1]), scale2, off2), a, b);
+    a = ex2(a);
+    b = ex2(b);
+    sum[j & 1] = add2(sum[j & 1], pair(a, b));
+    pk[j] = SH::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
+  }
+}
+
 // Stream w, lane row r.  False if a wait gave up.
 template <class SH>
-__device__ bool softmax(const PrefixParams& p, const PrefixTile& t, int n_tiles, bool two_rows,
-                        int w, int r, float sl2, uint8_t* ring, Ctl* ctl, uint32_t tmem, float& m,
-                        float& l) {
+__device__ __forceinline__ bool softmax(const PrefixParams& p, const PrefixTile& t, int n_tiles, bool two_rows,
+                                        int w, int r, float sl2, uint8_t* data, Ctl* ctl, float& m, float& l) {
   constexpr int D = SH::D;
   const int lane = r & 31;
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
-  const uint32_t sc = tmem + lanes + w * kTok, oc = tmem + lanes + kOCol + w * D;
+  const uint32_t sc = lanes + w * kTok, oc = lanes + kOCol + w * D;
   const int log2_page = p.log2_page;
   const bool pages = p.table != nullptr && p.page_size < kTok;
   const int step = two_rows ? 1 : 2;
+  const uint64_t scale2 = pair(sl2, sl2);
   m = kNegInf;
   l = 0.f;
-  for (int n = two_rows ? 0 : w, i = 0; n < n_tiles; n += step, ++i) {
+  int left = (int)(t.hi - t.lo) - (two_rows ? 0 : w) * kTok;  // tokens from this tile on
+  for (int n = two_rows ? 0 : w, i = 0; n < n_tiles; n += step, ++i, left -= step * kTok) {
     if (!warp_wait(ctl, smem_addr(&ctl->s_full[w]), i & 1)) return false;
     tc_fence_after();
     float s[kTok];
-    ld128(sc, s);
-    const int64_t t0 = t.lo + (int64_t)n * kTok;
+    tc_ld32x2(sc, sc + 32, s);
+    tc_ld32x2(sc + 64, sc + 96, s + 64);
     const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[n & 7]);
-    const bool clean = t0 + kTok <= t.hi && bad == 0u;
-    if (!clean) {                   // past the prompt's end, or on an invalid page: no weight
-      const int live = (int)min((int64_t)kTok, t.hi - t0);
+    if (left < kTok || bad != 0u) { // past the prompt's end, or on an invalid page: no weight
 #pragma unroll
       for (int j = 0; j < kTok; ++j) {
-        const bool out = j >= live || ((bad >> (pages ? j >> log2_page : 0)) & 1u);
+        const bool out = j >= left || ((bad >> (pages ? j >> log2_page : 0)) & 1u);
         s[j] = out ? kNegInf : s[j];
       }
       if constexpr (!SH::FP8) {     // (widen() has cleared them)
         // Their V rows may hold anything, and 0 * NaN would reach O: clear them.
-        const int e = 2 * n + 1;
-        if (!warp_wait(ctl, smem_addr(&ctl->full[e % SH::STAGES]), (e / SH::STAGES) & 1)) return false;
-        if (r >= live || ((bad >> (pages ? r >> log2_page : 0)) & 1u)) {
-          uint8_t* v = ring + (size_t)(e % SH::STAGES) * SH::TILE_BYTES + r * 128;
+        const int e = 2 * n + 1, stages = SH::stages(two_rows);
+        if (!warp_wait(ctl, smem_addr(&ctl->full[e % stages]), (e / stages) & 1)) return false;
+        if (r >= left || ((bad >> (pages ? r >> log2_page : 0)) & 1u)) {
+          uint8_t* v = data + SH::ring_off(two_rows) + (size_t)(e % stages) * SH::TILE_BYTES + r * 128;
 #pragma unroll
           for (int c = 0; c < SH::SLABS * 8; ++c)
             *reinterpret_cast<uint4*>(v + (c >> 3) * SH::SLAB_BYTES + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -375,13 +424,18 @@ __device__ bool softmax(const PrefixParams& p, const PrefixTile& t, int n_tiles,
         mx[k] = j + 4 + k < kTok ? max3(mx[k], s[j + k], s[j + 4 + k]) : fmaxf(mx[k], s[j + k]);
     }
     const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-    const float mn = fmaxf(m, mt);
-    const bool resc = i > 0 && m != kNegInf && mn > m + 8.f;
-    const float mu = (m == kNegInf || resc) ? mn : m;
-    if (__any_sync(0xffffffffu, resc)) {
+    // A row without a key so far takes this tile's maximum (there is nothing to rescale).
+    float base = m == kNegInf ? (mt == kNegInf ? 0.f : mt) : m;
+    uint32_t pk[32];
+    uint64_t sum[2] = {0ull, 0ull};
+    weights<SH>(s, scale2, pair(-base, -base), pk, sum);
+    const bool grows = m != kNegInf && mt > m + 8.f;
+    if (m == kNegInf) m = mt;
+    if (__any_sync(0xffffffffu, grows)) {
       // S of this tile is complete, so the product before it is too: O is stable.
-      const float c = resc ? ex2(m - mn) : 1.f;
+      const float c = grows ? ex2(m - mt) : 1.f;
       l *= c;
+      if (grows) base = m = mt;
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float o[32];
@@ -390,31 +444,19 @@ __device__ bool softmax(const PrefixParams& p, const PrefixTile& t, int n_tiles,
         for (int j = 0; j < 32; ++j) o[j] *= c;
         tc_st32(oc + q * 32, o);
       }
+      sum[0] = sum[1] = 0ull;
+      weights<SH>(s, scale2, pair(-base, -base), pk, sum);
     }
-    m = mu;
-    const float base = mu == kNegInf ? 0.f : mu;
-    const uint64_t scale2 = pair(sl2, sl2), off2 = pair(-base, -base);
-    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint32_t pk[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int k = half * 64 + 2 * j;
-        float a, b;
-        unpair(fma2(pair(s[k], s[k + 1]), scale2, off2), a, b);
-        a = ex2(a);
-        b = ex2(b);
-        sum[j & 3] = add2(sum[j & 3], pair(a, b));
-        pk[j] = SH::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
-      }
+      if (half == 1) weights<SH>(s + 64, scale2, pair(-base, -base), pk, sum);
       tc_st32w(sc + half * 32, pk);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&ctl->p_half[w][half]));
     }
     float a, b;
-    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+    unpair(add2(sum[0], sum[1]), a, b);
     l += a + b;
   }
   const bool any = two_rows || w < n_tiles;
@@ -430,9 +472,9 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // Two row tiles: a thread writes its row.
 template <int D>
-__device__ void write_rows(const PrefixParams& p, const PrefixTile& t, int g, int split, int w,
-                           int r, float m, float l, float vscale, uint32_t tmem) {
-  const uint32_t oc = tmem + ((uint32_t)(r & ~31) << 16) + kOCol + w * D;
+__device__ void write_rows(const PrefixParams& p, const PrefixTile& t, int g, int split, int w, int r, float m,
+                           float l, float vscale) {
+  const uint32_t oc = ((uint32_t)(r & ~31) << 16) + kOCol + w * D;
   const bool mine = w * kRows + r < t.rows;
   const int64_t at = mine ? prefix_flat_row(p, t, g, w * kRows + r) * p.S + split : 0;
   const float f = vscale / l;
@@ -452,59 +494,38 @@ __device__ void write_rows(const PrefixParams& p, const PrefixTile& t, int g, in
 }
 
 // Two streams of the same rows: merge them (M = max m, c = 2^(m - M), O = sum c O / sum c l).
-// Warpgroup w forms dims w d/2 .. of every row: each hands the other half of its own O over
-// in the drained ring, rows padded to 16-byte groups that fall into different banks.
+// Both streams' O of a row lie in its TMEM lane: either thread of the row forms half the dims.
 template <int D>
-__device__ void merge_rows(const PrefixParams& p, const PrefixTile& t, int g, int split, int n_tiles,
-                           int w, int r, float m, float l, float vscale, uint8_t* ring, Ctl* ctl,
-                           uint32_t tmem) {
-  constexpr int HALF = D / 2, LD = HALF + 4;
-  const uint32_t oc = tmem + ((uint32_t)(r & ~31) << 16) + kOCol + w * D;
-  float2* stats = reinterpret_cast<float2*>(ring + 2 * kRows * LD * sizeof(float));
-  stats[w * kRows + r] = make_float2(m, l);
-  named_bar_sync(1, 256);
-  const float m0 = stats[r].x, m1 = stats[kRows + r].x, M = fmaxf(m0, m1);
-  const float l0 = stats[r].y, l1 = stats[kRows + r].y;
-  const float c0 = l0 == 0.f ? 0.f : M == kNegInf ? 1.f : ex2(m0 - M);
-  const float c1 = l1 == 0.f ? 0.f : M == kNegInf ? 1.f : ex2(m1 - M);
-  const float L = l0 * c0 + l1 * c1;
-  const float c = w ? c1 : c0;
-  const bool has = w < n_tiles;               // a split of one tile has no second stream
-  float* theirs = reinterpret_cast<float*>(ring) + (size_t)((w ^ 1) * kRows + r) * LD;
-  const float* given = reinterpret_cast<const float*>(ring) + (size_t)(w * kRows + r) * LD;
+__device__ void merge_rows(const PrefixParams& p, const PrefixTile& t, int g, int split, int n_tiles, int half,
+                           int r, const float (&m)[2], const float (&l)[2], float vscale) {
+  const uint32_t oc = ((uint32_t)(r & ~31) << 16) + kOCol + half * (D / 2);
+  const float M = fmaxf(m[0], m[1]);
+  float c[2];
 #pragma unroll
-  for (int q = 0; q < HALF / 32; ++q) {
-    float o[32];
-    if (has) tc_ld32(oc + (w ^ 1) * HALF + q * 32, o);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) o[j] = has && c != 0.f ? o[j] * c : 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4)
-      *reinterpret_cast<float4*>(theirs + q * 32 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-  }
-  named_bar_sync(1, 256);
+  for (int w = 0; w < 2; ++w) c[w] = l[w] == 0.f ? 0.f : M == kNegInf ? 1.f : ex2(m[w] - M);
+  const float L = l[0] * c[0] + l[1] * c[1], f = vscale / L;
   const bool mine = r < t.rows;
   const int64_t at = mine ? prefix_flat_row(p, t, g, r) * p.S + split : 0;
-  const float f = vscale / L;
 #pragma unroll
-  for (int q = 0; q < HALF / 32; ++q) {
+  for (int q = 0; q < D / 64; ++q) {
     float o[32];
-    __syncwarp();
-    if (has) tc_ld32(oc + w * HALF + q * 32, o);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if (w >= n_tiles) continue;             // a split of one tile has no second stream
+      float x[32];
+      __syncwarp();
+      tc_ld32(oc + w * D + q * 32, x);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = c[w] != 0.f ? fmaf(x[j], c[w] * f, o[j]) : o[j];
+    }
     if (mine && L != 0.f) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(given + q * 32 + j);
-        o[j] = ((has && c != 0.f ? o[j] * c : 0.f) + x.x) * f;
-        o[j + 1] = ((has && c != 0.f ? o[j + 1] * c : 0.f) + x.y) * f;
-        o[j + 2] = ((has && c != 0.f ? o[j + 2] * c : 0.f) + x.z) * f;
-        o[j + 3] = ((has && c != 0.f ? o[j + 3] * c : 0.f) + x.w) * f;
-      }
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) store8(p.o_part + at * D + w * HALF + q * 32 + j, o + j);
+      for (int j = 0; j < 32; j += 8) store8(p.o_part + at * D + half * (D / 2) + q * 32 + j, o + j);
     }
   }
-  if (mine && w == 0) p.lse_part[at] = lse_of(M, L);
+  if (mine && half == 0) p.lse_part[at] = lse_of(M, L);
 }
 
 template <class SH>
@@ -512,17 +533,14 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
     fd_prefix_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const __grid_constant__ PrefixParams p) {
   constexpr int D = SH::D;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* ring = base + SH::RING_OFF;
+  extern __shared__ __align__(1024) uint8_t base[];   // whole swizzle atoms
   Ctl* ctl = reinterpret_cast<Ctl*>(base + SH::CTL_OFF);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, g = blockIdx.y;
   if (tid == 0) {
-    for (int s = 0; s < SH::STAGES; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_addr(&ctl->full[s]), SH::FP8 ? 4 : 1);   // FP8: the widening warps arrive
-      mbar_init(smem_addr(&ctl->empty[s]), 1);
+      mbar_init(smem_addr(&ctl->empty[s]), 2);
     }
     for (int s = 0; SH::FP8 && s < 4; ++s) {
       mbar_init(smem_addr(&ctl->raw_full[s]), 1);
@@ -534,7 +552,7 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       mbar_init(smem_addr(&ctl->p_half[w][1]), 4);
       mbar_init(smem_addr(&ctl->o_full[w]), 1);
     }
-    mbar_init(smem_addr(&ctl->mma_done), 1);
+    mbar_init(smem_addr(&ctl->mma_done), 2);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -557,7 +575,6 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
   const bool found = ctl->found != 0;
   const PrefixTile t = ctl->tile;
   const int n_tiles = found && t.lo < t.hi ? (int)((t.hi - t.lo + kTok - 1) / kTok) : 0;
@@ -565,7 +582,7 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
   const int raw_stages = two_rows ? 2 : 4;
 
   if (n_tiles > 0) {
-    // Registers of the warpgroups (softmax, softmax, producer and issuer, widening): 216 +
+    // Registers of the warpgroups (softmax, softmax, producer and issuers, widening): 216 +
     // 216 + 72 is what three were launched with (168 each), 184 + 184 + 56 + 88 four (128).
     if (warp >= 12) {
       if constexpr (SH::FP8) {
@@ -576,11 +593,10 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       if constexpr (SH::FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp == 8) {
-        produce<SH>(p, t, g, n_tiles, raw_stages, &tk, &tv, smem_addr(base), ctl, lane);
-      } else if (warp == 9) {
-        named_bar_sync(2, 288);               // Q is in place
-        if (lane == 0) issue<SH>(p, n_tiles, two_rows, smem_addr(base), smem_addr(ring), ctl, tmem);
-        __syncwarp();
+        produce<SH>(p, t, g, n_tiles, raw_stages, two_rows, &tk, &tv, smem_addr(base), ctl, lane);
+      } else if (warp < 11) {
+        named_bar_sync(2, 320);               // Q is in place
+        issue<SH>(p, warp - 9, n_tiles, two_rows, smem_addr(base), ctl);
       }
     } else {
       if constexpr (SH::FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
@@ -615,19 +631,23 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
         }
       }
       fence_proxy_async_smem();
-      named_bar_sync(2, 288);
+      named_bar_sync(2, 320);
       float m, l;
-      if (!softmax<SH>(p, t, n_tiles, two_rows, w, r, sl2, ring, ctl, tmem, m, l) && lane == 0)
-        set_abort(p, ctl);
+      if (!softmax<SH>(p, t, n_tiles, two_rows, w, r, sl2, base, ctl, m, l) && lane == 0) set_abort(p, ctl);
       named_bar_sync(1, 256);                 // both streams are done, or one gave up
+      float2* stats = reinterpret_cast<float2*>(base);        // Q is not needed any more
+      stats[w * kRows + r] = make_float2(m, l);
+      named_bar_sync(1, 256);
       if (aborted(ctl)) {
         const int row = two_rows ? w * kRows + r : r;
         if (row < t.rows && (two_rows || w == 0))
           p.lse_part[prefix_flat_row(p, t, g, row) * p.S + split] = kNegInf;
       } else if (two_rows) {
-        write_rows<D>(p, t, g, split, w, r, m, l, vs, tmem);
+        write_rows<D>(p, t, g, split, w, r, m, l, vs);
       } else {
-        merge_rows<D>(p, t, g, split, n_tiles, w, r, m, l, vs, ring, ctl, tmem);
+        const float2 a = stats[r], b = stats[kRows + r];
+        const float ms[2] = {a.x, b.x}, ls[2] = {a.y, b.y};
+        merge_rows<D>(p, t, g, split, n_tiles, w, r, ms, ls, vs);
       }
     }
   } else if (found) {               // nothing of the prompt in this split
@@ -638,7 +658,7 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
   pdl_trigger();
   if (warp == 9) {
     tc_fence_after();
-    tc_dealloc(tmem, kCols);
+    tc_dealloc(ctl->tmem, kCols);
   }
 }
 
