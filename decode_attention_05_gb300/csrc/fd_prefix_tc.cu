@@ -82,6 +82,7 @@ struct Ctl {
   uint64_t s_full[2];                             // S of the stream's next tile is complete
   uint64_t p_half[2][2];                          // the first / second 64 tokens of P are in place
   uint64_t o_full[2];                             // the stream's last product is complete
+  uint64_t turn[2];                               // the other stream's products have been issued
   uint64_t mma_done;                              // all products of the CTA are complete
   uint32_t bad[8];                                // tile n mod 8: bit j = its page j is invalid
   int32_t abort, found;
@@ -297,60 +298,66 @@ __device__ __forceinline__ void issue(const PrefixParams& p, int w, int n_tiles_
   if (!two_rows && w == 1) advance(ks, kp, 2);
   vs = ks, vp = kp;
   advance(vs, vp, 1);
-  // A ring entry is free once both issuers have committed to it: with one row tile its only
-  // user does so twice.
+  // What follows is issued by the elected lane.  A ring entry is free once both issuers have
+  // committed to it: with one row tile its only user does so twice.
   auto release = [&](int st) {
-    if (elected()) {
-      tc_commit(smem_addr(&ctl->empty[st]));
-      if (!two_rows) tc_commit(smem_addr(&ctl->empty[st]));
-    }
-    __syncwarp();
+    tc_commit(smem_addr(&ctl->empty[st]));
+    if (!two_rows) tc_commit(smem_addr(&ctl->empty[st]));
   };
   auto scores = [&]() {
     const uint64_t k = k0 + (uint32_t)ks * kTile16;
-    if (elected()) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t off = (i >> 2) * kSlab16 + (i & 3) * 2u;
-        tc_mma_ss(w * kTok, q + off, k + off, id_s, i > 0);
-      }
-      tc_commit(smem_addr(&ctl->s_full[w]));
+    for (int i = 0; i < D / 16; ++i) {
+      const uint32_t off = (i >> 2) * kSlab16 + (i & 3) * 2u;
+      tc_mma_ss(w * kTok, q + off, k + off, id_s, i > 0);
     }
-    __syncwarp();
-    release(ks);
-    advance(ks, kp, jump);
   };
   bool ok = true;
   const int first = two_rows ? 0 : w;
   if (first < n_tiles) {
     ok = warp_wait(ctl, smem_addr(&ctl->full[ks]), kp);
-    if (ok) scores();
+    if (ok && elected()) {
+      scores();
+      tc_commit(smem_addr(&ctl->s_full[w]));
+      release(ks);
+    }
+    __syncwarp();
+    advance(ks, kp, jump);
   }
   int i = 0;
   for (int n = first; n < n_tiles && ok; n += step, ++i) {
     const bool more = n + step < n_tiles;
-    ok = warp_wait(ctl, smem_addr(&ctl->full[vs]), vp);
-    const uint64_t v = v0 + (uint32_t)vs * kTile16;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      ok = ok && warp_wait(ctl, smem_addr(&ctl->p_half[w][half]), i & 1);
-      if (!ok) break;
-      tc_fence_after();
-      if (elected()) {
-#pragma unroll
-        for (int x = half * 4; x < half * 4 + 4; ++x)
-          tc_mma_ts(kOCol + w * D, w * kTok + x * 8, v + x * (2048u >> 4), id_o, (i > 0 || x > 0) ? 1u : 0u);
-        if (half == 1 && !more) tc_commit(smem_addr(&ctl->o_full[w]));
-      }
-      __syncwarp();
-    }
+    // Everything but the second half of P before this stream's turn: even a wait that is over
+    // takes over a hundred cycles, in which the tensor cores would run dry.  The streams take
+    // turns so that they stay out of step, one's products under the other's softmax.
+    ok = warp_wait(ctl, smem_addr(&ctl->full[vs]), vp) &&
+         (!more || warp_wait(ctl, smem_addr(&ctl->full[ks]), kp)) &&
+         warp_wait(ctl, smem_addr(&ctl->p_half[w][0]), i & 1) &&
+         ((w == 0 && i == 0) || warp_wait(ctl, smem_addr(&ctl->turn[w]), (w ? i : i - 1) & 1));
     if (!ok) break;
-    if (more) {
-      ok = warp_wait(ctl, smem_addr(&ctl->full[ks]), kp);
-      if (!ok) break;
-      scores();                     // S of the next tile is complete behind P V
+    const uint64_t v = v0 + (uint32_t)vs * kTile16;
+    auto outputs = [&](int half) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        tc_mma_ts(kOCol + w * D, w * kTok + (half * 4 + x) * 8, v + (half * 4 + x) * (2048u >> 4), id_o,
+                  (i > 0 || half + x > 0) ? 1u : 0u);
+    };
+    tc_fence_after();
+    if (elected()) outputs(0);
+    __syncwarp();
+    ok = warp_wait(ctl, smem_addr(&ctl->p_half[w][1]), i & 1);
+    if (!ok) break;
+    tc_fence_after();
+    if (elected()) {
+      outputs(1);
+      if (more) scores();
+      mbar_arrive(smem_addr(&ctl->turn[w ^ 1]));
+      tc_commit(smem_addr(more ? &ctl->s_full[w] : &ctl->o_full[w]));   // S is complete behind P V
+      if (more) release(ks);
+      release(vs);
     }
-    release(vs);
+    __syncwarp();
+    if (more) advance(ks, kp, jump);
     advance(vs, vp, jump);
   }
   if (!ok && elected()) set_abort(p, ctl);
@@ -551,6 +558,7 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       mbar_init(smem_addr(&ctl->p_half[w][0]), 4);
       mbar_init(smem_addr(&ctl->p_half[w][1]), 4);
       mbar_init(smem_addr(&ctl->o_full[w]), 1);
+      mbar_init(smem_addr(&ctl->turn[w]), 1);
     }
     mbar_init(smem_addr(&ctl->mma_done), 2);
     ctl->abort = 0;
