@@ -47,6 +47,18 @@ Layout layout(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d, int32_t 
   return w;
 }
 
+// Splits of the rows' own keys: the count of a plain decode call, and more where that call
+// would run head-group tiles (small pages; four kv heads a CTA) on few rows.  A plain call's
+// rows are long then; here the own part is short, and one split of a quarter of the kv heads
+// leaves most SMs without work (32 rows of up to 1024 tokens, 16-token pages: 49 us with one).
+int32_t own_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d, int64_t L_cap, int32_t num_splits) {
+  const int32_t s = fd_resolve_num_splits_q(B, Q, Hq, Hkv, d, L_cap, num_splits);
+  if (num_splits > 0 || d != 128 || Hkv % fd::kHeadGroup != 0 || Q * (Hq / Hkv) > fd::kMaxNarrowRows) return s;
+  const int64_t ctas = (int64_t)B * Hkv / fd::kHeadGroup, sms = fd::sm_count();
+  const int64_t want = std::min((2 * sms + ctas - 1) / ctas, (L_cap + 127) / 128);
+  return (int32_t)std::max<int64_t>(s, std::min<int64_t>(want, kMaxSplits));
+}
+
 }  // namespace
 
 extern "C" {
@@ -71,7 +83,7 @@ size_t fd_shared_prefix_workspace_size(int32_t B, int32_t Q, int32_t Hq, int32_t
     return 0;
   return layout(B, Q, Hq, Hkv, d,
                 fd_resolve_prefix_splits(B, Q, Hq, Hkv, P, L_prefix_cap, prefix_splits),
-                fd_resolve_num_splits_q(B, Q, Hq, Hkv, d, L_cap, num_splits))
+                own_splits(B, Q, Hq, Hkv, d, L_cap, num_splits))
       .total;
 }
 
@@ -170,8 +182,7 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   const int64_t L_cap = block_table ? block_table->shape[1] * page_size : k_cache->shape[2];
   const int32_t Sp = fd_resolve_prefix_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv,
                                               (int32_t)P, Lp, prefix_splits);
-  const int32_t S = fd_resolve_num_splits_q((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv,
-                                            (int32_t)d, L_cap, num_splits);
+  const int32_t S = own_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv, (int32_t)d, L_cap, num_splits);
   if (((uintptr_t)workspace & (kAlign - 1)) != 0) return bad("workspace must be 256-byte aligned");
   const Layout wl = layout((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv, (int32_t)d, Sp, S);
   if (workspace_bytes < wl.total)

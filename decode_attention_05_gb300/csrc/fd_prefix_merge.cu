@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(kWarps * 32) fd_prefix_merge_kernel(const __gr
 
 template <int D>
 cudaError_t launch(const MergeParams& p, cudaStream_t stream) {
-  // A warp per row once that fills the GPU's SMs several times over; before that four warps
+  // A warp per row once that gives every SM a few rows to overlap; before that four warps
   // share a row, whose loads then run side by side.
-  if (p.rows >= 16 * (int64_t)sm_count() && p.S[0] + p.S[1] <= kBatch)
+  if (p.rows >= 8 * (int64_t)sm_count())
     return launch_pdl(fd_prefix_merge_kernel<D, 1>, dim3((unsigned)((p.rows + kWarps - 1) / kWarps)),
                       kWarps * 32, 0, stream, p);
   return launch_pdl(fd_prefix_merge_kernel<D, kWarps>, dim3((unsigned)p.rows), kWarps * 32, 0, stream, p);
