@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -142,10 +143,11 @@ def _declare(L):
     L.fd_plan_destroy.restype = None
     L.fd_plan_destroy.argtypes = [vp]
     L.fd_append_kv.restype = ctypes.c_int
-    L.fd_append_kv.argtypes = [P, P, P, vp, vp, P, i32, vp, P, P, P, vp, vp, P, i32, vp, vp]
+    # (tensors as packed bytes: see _packed)
+    L.fd_append_kv.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
     L.fd_decode_shared_prefix.restype = ctypes.c_int
-    L.fd_decode_shared_prefix.argtypes = [P, P, P, vp, vp, P, P, P, vp, vp, vp, P, i32, i32, i32,
-                                          P, vp, vp, sz, vp, O]
+    L.fd_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32,
+                                          i32, i32, vp, vp, vp, sz, vp, O]
     L.fd_shared_prefix_workspace_size.restype = sz
     L.fd_shared_prefix_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i64, i64, i32, i32]
     L.fd_resolve_prefix_splits.restype = i32
@@ -489,6 +491,26 @@ def merge_partials(lse_part: torch.Tensor, o_part: torch.Tensor, out: Optional[t
     return out, lse_out
 
 
+# An fd_tensor of n dims as struct.pack lays it out: building the ctypes structure field by
+# field costs several microseconds a tensor, more than a small call takes on the GPU.
+_LAYOUT = [struct.Struct("Pii" + ("%dq%dx" % (n, 8 * (4 - n))) * 2).pack if n else None
+           for n in range(5)]
+
+
+def _packed(t: Optional[torch.Tensor]) -> Optional[bytes]:
+    """The bytes of a tensor's fd_tensor (None stays None)."""
+    if t is None:
+        return None
+    shape = t.shape
+    n = len(shape)
+    if not 1 <= n <= 4:
+        raise ValueError("fd_tensor holds 1 to 4 dims")
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    return _LAYOUT[n](t.data_ptr(), dtype, n, *shape, *t.stride())
+
+
 def _ints(t: Optional[torch.Tensor], name: str) -> Optional[int]:
     """Address of a contiguous int32 tensor (None stays None)."""
     if t is None:
@@ -504,6 +526,26 @@ def _floats(t: Optional[torch.Tensor], name: str) -> Optional[int]:
     if t.dtype != torch.float32 or not t.is_contiguous():
         raise TypeError("%s must be a contiguous float32 tensor" % name)
     return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_place(stream, *tensors) -> Optional[int]:
+    """The stream to launch on, after a check that every tensor is on the current device (an
+    address of another device, or of the host, would be read by the wrong one)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors are on different devices")
+    if dev >= 0:
+        if dev != torch.cuda.current_device():
+            raise ValueError("the tensors are on cuda:%d, which is not the current device" % dev)
+        if stream is None and _raw_stream is not None:
+            return _raw_stream(dev) or None
+    elif torch.cuda.is_available():
+        raise ValueError("the tensors are not on a CUDA device")
+    return _stream_handle(stream)
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -537,14 +579,18 @@ def append_kv(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     for s in (k_scale, v_scale):
         if s is not None and s.numel() != k_cache.shape[1]:
             raise ValueError("scales need one entry per kv head")
-    dq, dk, dv, do = tensor_desc(q), tensor_desc(k), tensor_desc(v), tensor_desc(q_out)
-    dkc, dvc, dcs, dbt = (tensor_desc(k_cache), tensor_desc(v_cache), tensor_desc(cos_sin),
-                          tensor_desc(block_table))
-    _check(lib().fd_append_kv(
-        _ref(dq), _ref(dk), _ref(dv), _ints(cu_tokens, "cu_tokens"), _ints(seq_lens, "seq_lens"),
-        _ref(dcs), rope_style, _ints(pos_offset, "pos_offset"), _ref(do), _ref(dkc), _ref(dvc),
-        _floats(k_scale, "k_scale"), _floats(v_scale, "v_scale"), _ref(dbt), page_size,
-        None if workspace is None else workspace.data_ptr(), _stream_handle(stream)))
+    if workspace is not None and workspace.numel() * workspace.element_size() < 256:
+        raise ValueError("the workspace's header needs 256 bytes")
+    place = _launch_place(stream, k, v, q, q_out, k_cache, v_cache, seq_lens, cos_sin, pos_offset,
+                          cu_tokens, block_table, k_scale, v_scale, workspace)
+    status = lib().fd_append_kv(
+        _packed(q), _packed(k), _packed(v), _ints(cu_tokens, "cu_tokens"),
+        _ints(seq_lens, "seq_lens"), _packed(cos_sin), rope_style,
+        _ints(pos_offset, "pos_offset"), _packed(q_out), _packed(k_cache), _packed(v_cache),
+        _floats(k_scale, "k_scale"), _floats(v_scale, "v_scale"), _packed(block_table), page_size,
+        None if workspace is None else workspace.data_ptr(), place)
+    if status != FD_OK:
+        _check(status)
     return q_out
 
 
@@ -596,17 +642,18 @@ def decode_attention_shared_prefix(
             B, Qn, Hq, k_cache.shape[1], d, P, _cap(k_prefix, prefix_table, page_size),
             _cap(k_cache, block_table, page_size), prefix_splits, num_splits),
             dtype=torch.uint8, device=q.device)
-    dq, dkp, dvp, dpt = (tensor_desc(q), tensor_desc(k_prefix), tensor_desc(v_prefix),
-                         tensor_desc(prefix_table))
-    dk, dv, dbt, do = (tensor_desc(k_cache), tensor_desc(v_cache), tensor_desc(block_table),
-                       tensor_desc(out))
-    _check(lib().fd_decode_shared_prefix(
-        _ref(dq), _ref(dkp), _ref(dvp), _ints(prefix_lens, "prefix_lens"),
-        _ints(group_start, "group_start"), _ref(dpt), _ref(dk), _ref(dv),
-        _floats(k_scale, "k_scale"), _floats(v_scale, "v_scale"), _ints(seq_lens, "seq_lens"),
-        _ref(dbt), page_size, prefix_splits, num_splits, _ref(do), lse_out.data_ptr(),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream_handle(stream), _ref(options)))
+    place = _launch_place(stream, q, k_prefix, v_prefix, prefix_lens, group_start, prefix_table,
+                          k_cache, v_cache, seq_lens, block_table, k_scale, v_scale, out, lse_out,
+                          workspace)
+    status = lib().fd_decode_shared_prefix(
+        _packed(q), _packed(k_prefix), _packed(v_prefix), _ints(prefix_lens, "prefix_lens"),
+        _ints(group_start, "group_start"), _packed(prefix_table), _packed(k_cache),
+        _packed(v_cache), _floats(k_scale, "k_scale"), _floats(v_scale, "v_scale"),
+        _ints(seq_lens, "seq_lens"), _packed(block_table), page_size, prefix_splits, num_splits,
+        _packed(out), lse_out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), place, _ref(options))
+    if status != FD_OK:
+        _check(status)
     return out, lse_out
 
 

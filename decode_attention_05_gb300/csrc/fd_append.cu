@@ -56,16 +56,31 @@ __device__ __forceinline__ void flag(const AppendParams& p, uint32_t f) {
   if (p.flags != nullptr) atomicOr(p.flags, f);
 }
 
-// Eight consecutive elements in f32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* a, float* x) {
-  const uint4 r = *reinterpret_cast<const uint4*>(a);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight consecutive elements as they lie in memory (half the registers of f32 for bf16, which
+// is what decides how many loads an SM has in flight), and widened to f32.
+template <class T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* a) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16lo_to_f32(w[i]);
-    x[2 * i + 1] = bf16hi_to_f32(w[i]);
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(a) + i);
   }
-}
+  __device__ __forceinline__ void widen(float* x) const {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          x[2 * j] = bf16lo_to_f32(w[j]);
+          x[2 * j + 1] = bf16hi_to_f32(w[j]);
+        } else {
+          x[4 * i + j] = __uint_as_float(w[j]);
+        }
+      }
+    }
+  }
+};
 __device__ __forceinline__ void load8(const float* a, float* x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -121,7 +136,7 @@ constexpr int kAppendThreads = 128;
 // TI: q, k, v and q_out; TC: the caches.  A warp takes ITER x 32 / (D / 16) head rows
 // of one token; rows are numbered q heads first, then k, then v.
 template <class TI, class TC, int D, int ITER>
-__global__ void __launch_bounds__(kAppendThreads) fd_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, ITER == 1 ? 9 : sizeof(TI) == 2 ? 6 : 4) fd_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int TPR = D / 16;                 // threads per head row
   constexpr int RPW = 32 / TPR;               // rows of a warp at once
   pdl_trigger();
@@ -145,7 +160,7 @@ __global__ void __launch_bounds__(kAppendThreads) fd_append_kernel(const __grid_
   // The inputs, before anything is known of the token's place.
   const int tb = p.cu_tokens == nullptr ? t / p.Q : 0;         // batch row of a 4-D input
   const int tj = p.cu_tokens == nullptr ? t - tb * p.Q : t;
-  float x0[ITER][8], x1[ITER][8];
+  Raw8<TI> x0[ITER], x1[ITER];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     const int r = r0 + i * RPW;
@@ -160,8 +175,8 @@ __global__ void __launch_bounds__(kAppendThreads) fd_append_kernel(const __grid_
     }
     // v rows are stored as they are: their groups need not follow the pairs, but a common
     // layout keeps the warp in step.
-    load8(src + e0, x0[i]);
-    load8(src + e1, x1[i]);
+    x0[i].load(src + e0);
+    x1[i].load(src + e1);
   }
 
   // The token's row, position and slot.
@@ -212,8 +227,9 @@ __global__ void __launch_bounds__(kAppendThreads) fd_append_kernel(const __grid_
   for (int i = 0; i < ITER; ++i) {
     const int r = r0 + i * RPW;
     if (r >= n_rows) continue;
-    float* a = x0[i];
-    float* h = x1[i];
+    float a[8], h[8];
+    x0[i].widen(a);
+    x1[i].widen(h);
     if (turned && r < vbase) {
       if (p.interleaved) {
 #pragma unroll

@@ -1,12 +1,17 @@
 // fd_prefix_simt.cu -- attention of many query rows over a shared prompt, on CUDA cores
-// (fd_prefix.cuh says what the pass computes).
+// (fd_prefix.cuh says what the pass computes): f32 inputs, and bf16 as a cross-check.
 //
 // A CTA holds 64 query rows of one group and kv head and walks its split of the prompt in
-// tiles of 32 tokens: S = Q K^T, the running maximum and sum of the softmax ("AI Infra: math
+// tiles of 64 tokens: S = Q K^T, the running maximum and sum of the softmax ("AI Infra: math
 // and infra optimisation in large models", section 2.6), O = O 2^(m_old - m_new) + P V.  All
 // in f32.  256 threads: thread (ty, tx) of a 16 x 16 grid has the scores of rows 4 ty .. + 3
-// and tokens 2 tx, 2 tx + 1, and the outputs of the same rows and D / 16 dims, so a row's 16
+// and tokens tx + 16 j (j < 4), and the outputs of the same rows and D / 16 dims, so a row's 16
 // threads lie in one half warp and reduce with shuffles.
+//
+// Bound: the FMA pipes.  Every 16-byte read of shared memory feeds 8 FMAs of the scores (10 of
+// the outputs at D = 128), rows are padded by 16 bytes so that neither the tokens' rows nor P's
+// columns collide in banks, and the next tile's rows are in registers while the current one is
+// worked on.  K and V take turns in one buffer, which leaves room for two CTAs per SM.
 #include <cuda_bf16.h>
 
 #include "fd_prefix.cuh"
@@ -14,33 +19,34 @@
 namespace fd {
 namespace {
 
-constexpr int kBM = 64, kBN = 32, kThreads = 256;
-constexpr int kQs = kBM + 4, kKs = kBN + 4, kPs = kBM + 4;   // padded leading dimensions
+constexpr int kBM = 64, kBN = 64, kThreads = 256;
+constexpr int kPs = kBM + 4;        // padded leading dimension of P
 
 template <int D>
-constexpr size_t smem_bytes() {
-  return (size_t)(D * kQs + D * kKs + kBN * D + kBN * kPs) * sizeof(float);
-}
+struct Smem {
+  static constexpr int LD = D + 4;
+  float q[kBM * LD];
+  float kv[kBN * LD];               // the tile's K, then its V
+  float p[kBN * kPs];
+  float mask[kBN];                  // 0, or -inf for a token without weight
+  PrefixTile tile;
+  int found;
+};
 
-__device__ __forceinline__ void load4(const float* a, float* x) {
-  const float4 r = *reinterpret_cast<const float4*>(a);
-  x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* a, float* x) {
+__device__ __forceinline__ float4 load4(const float* a) { return *reinterpret_cast<const float4*>(a); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* a) {
   const uint2 r = *reinterpret_cast<const uint2*>(a);
-  x[0] = bf16lo_to_f32(r.x), x[1] = bf16hi_to_f32(r.x);
-  x[2] = bf16lo_to_f32(r.y), x[3] = bf16hi_to_f32(r.y);
+  return make_float4(bf16lo_to_f32(r.x), bf16hi_to_f32(r.x), bf16lo_to_f32(r.y), bf16hi_to_f32(r.y));
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_constant__ PrefixParams p) {
-  extern __shared__ __align__(16) float smem[];
-  float* qs = smem;                 // [D][kQs], rows of the tile along the last index
-  float* ks = qs + D * kQs;         // [D][kKs]
-  float* vs = ks + D * kKs;         // [kBN][D]
-  float* ps = vs + kBN * D;         // [kBN][kPs]
-  __shared__ PrefixTile tile;
-  __shared__ int found;
+__global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __grid_constant__ PrefixParams p) {
+  using SM = Smem<D>;
+  constexpr int LD = SM::LD, DV = D / 16;
+  constexpr int RPT = kThreads / (D / 4);      // tile rows that the threads load at once
+  constexpr int NR = kBN / RPT;                // ... and how often
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SM& sm = *reinterpret_cast<SM*>(smem_raw);
   pdl_wait();
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int split = blockIdx.x, g = blockIdx.y;
@@ -49,26 +55,57 @@ __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_c
     const bool ok = find_tile<kBM>(p, (int)blockIdx.z, t);
     if (ok) split_of<kBN>(p, split, t);
     if (tid == 0) {
-      tile = t;
-      found = ok ? 1 : 0;
+      sm.tile = t;
+      sm.found = ok ? 1 : 0;
     }
   }
   __syncthreads();
-  if (!found) return;
-  const PrefixTile t = tile;
+  if (!sm.found) return;
+  const PrefixTile t = sm.tile;
   if (t.lo >= t.hi) {               // nothing of the prompt in this split
     if (tid < t.rows) p.lse_part[prefix_flat_row(p, t, g, tid) * p.S + split] = kNegInf;
     return;
   }
-  for (int i = tid; i < kBM * (D / 4); i += kThreads) {
-    const int r = i % kBM, c = i / kBM;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < t.rows) load4(static_cast<const T*>(p.q) + prefix_q_offset(p, t, g, r) + c * 4, x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) qs[(c * 4 + e) * kQs + r] = x[e] * p.scale_log2;
+  const int lr = tid / (D / 4), lc = tid % (D / 4) * 4;   // this thread's row and dims of a load
+  for (int r = lr; r < kBM; r += RPT) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < t.rows) x = load4(static_cast<const T*>(p.q) + prefix_q_offset(p, t, g, r) + lc);
+    const float f = p.scale_log2;
+    *reinterpret_cast<float4*>(sm.q + r * LD + lc) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
   }
 
-  constexpr int DV = D / 16;
+  // Where the rows of a tile that this thread loads lie: page (or prompt) and slot, -1: none.
+  bool bad_page = false;
+  int64_t place[NR];
+  int32_t slot[NR];
+  auto locate = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int64_t tok = t0 + lr + i * RPT;
+      place[i] = t.group;
+      slot[i] = tok < t.hi ? (int32_t)tok : -1;
+      if (slot[i] >= 0 && p.table != nullptr) {
+        place[i] = p.table[(int64_t)t.group * p.table_sb + (tok >> p.log2_page)];
+        slot[i] = (int32_t)(tok & (p.page_size - 1));
+        if (place[i] < 0 || place[i] >= p.num_pages) {
+          slot[i] = -1;
+          bad_page = true;
+        }
+      }
+    }
+  };
+  float4 next[NR];
+  auto fetch = [&](const void* base, int64_t sb, int64_t sh, int64_t st) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      next[i] = slot[i] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : load4(static_cast<const T*>(base) + place[i] * sb + g * sh + slot[i] * st + lc);
+  };
+  auto store = [&] {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) *reinterpret_cast<float4*>(sm.kv + (lr + i * RPT) * LD + lc) = next[i];
+  };
+
   float m[4], l[4], acc[4][DV];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -77,73 +114,66 @@ __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_c
 #pragma unroll
     for (int e = 0; e < DV; ++e) acc[i][e] = 0.f;
   }
-  bool bad_page = false;
+  locate(t.lo);
+  fetch(p.k, p.k_sb, p.k_sh, p.k_st);
   for (int64_t t0 = t.lo; t0 < t.hi; t0 += kBN) {
-    __syncthreads();                // the previous tile has been read
-    for (int i = tid; i < kBN * (D / 4); i += kThreads) {
-      const int r = i % kBN, c = i / kBN;
-      const int64_t tok = t0 + r;
-      float kx[4] = {0.f, 0.f, 0.f, 0.f}, vx[4] = {0.f, 0.f, 0.f, 0.f};
-      bool live = tok < t.hi;
-      int64_t place = t.group, slot = tok;
-      if (live && p.table != nullptr) {
-        place = p.table[(int64_t)t.group * p.table_sb + (tok >> p.log2_page)];
-        slot = tok & (p.page_size - 1);
-        if (place < 0 || place >= p.num_pages) {
-          live = false;
-          bad_page = true;
-        }
-      }
-      if (live) {
-        load4(static_cast<const T*>(p.k) + place * p.k_sb + g * p.k_sh + slot * p.k_st + c * 4, kx);
-        load4(static_cast<const T*>(p.v) + place * p.v_sb + g * p.v_sh + slot * p.v_st + c * 4, vx);
-      }
+    store();                        // K of this tile
+    if (lc == 0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ks[(c * 4 + e) * kKs + r] = kx[e];
-      *reinterpret_cast<float4*>(vs + r * D + c * 4) = make_float4(vx[0], vx[1], vx[2], vx[3]);
-      if (c == 0) ps[r * kPs] = live ? 0.f : kNegInf;   // which tokens count, until P is written
+      for (int i = 0; i < NR; ++i) sm.mask[lr + i * RPT] = slot[i] < 0 ? kNegInf : 0.f;
     }
     __syncthreads();
-    float s[4][2] = {};
-#pragma unroll 8
-    for (int k = 0; k < D; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(qs + k * kQs + ty * 4);
-      const float2 b = *reinterpret_cast<const float2*>(ks + k * kKs + tx * 2);
-      s[0][0] = fmaf(a.x, b.x, s[0][0]), s[0][1] = fmaf(a.x, b.y, s[0][1]);
-      s[1][0] = fmaf(a.y, b.x, s[1][0]), s[1][1] = fmaf(a.y, b.y, s[1][1]);
-      s[2][0] = fmaf(a.z, b.x, s[2][0]), s[2][1] = fmaf(a.z, b.y, s[2][1]);
-      s[3][0] = fmaf(a.w, b.x, s[3][0]), s[3][1] = fmaf(a.w, b.y, s[3][1]);
+    fetch(p.v, p.v_sb, p.v_sh, p.v_st);
+    float s[4][4] = {};
+#pragma unroll 4
+    for (int k = 0; k < D; k += 4) {
+      float4 b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sm.kv + (tx + 16 * j) * LD + k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 a = *reinterpret_cast<const float4*>(sm.q + (ty * 4 + i) * LD + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[i][j] = fmaf(a.x, b[j].x, fmaf(a.y, b[j].y, fmaf(a.z, b[j].z, fmaf(a.w, b[j].w, s[i][j]))));
+      }
     }
-    const bool out0 = ps[(tx * 2) * kPs] == kNegInf, out1 = ps[(tx * 2 + 1) * kPs] == kNegInf;
-    float pr[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool out = sm.mask[tx + 16 * j] != 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i][j] = out ? kNegInf : s[i][j];
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s[i][0] = out0 ? kNegInf : s[i][0];
-      s[i][1] = out1 ? kNegInf : s[i][1];
-      float mt = fmaxf(s[i][0], s[i][1]);
+      float mt = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
       const float mn = fmaxf(m[i], mt);
       const float c = mn == kNegInf ? 1.f : ex2(m[i] - mn);
-      pr[i][0] = s[i][0] == kNegInf ? 0.f : ex2(s[i][0] - mn);
-      pr[i][1] = s[i][1] == kNegInf ? 0.f : ex2(s[i][1] - mn);
-      l[i] = l[i] * c + pr[i][0] + pr[i][1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = s[i][j] == kNegInf ? 0.f : ex2(s[i][j] - mn);
+      l[i] = l[i] * c + ((s[i][0] + s[i][1]) + (s[i][2] + s[i][3]));
 #pragma unroll
       for (int e = 0; e < DV; ++e) acc[i][e] *= c;
       m[i] = mn;
     }
-    __syncthreads();                // the marks have been read
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<float4*>(ps + (tx * 2 + j) * kPs + ty * 4) =
-          make_float4(pr[0][j], pr[1][j], pr[2][j], pr[3][j]);
-    __syncwarp();                   // a row's P is written and read by its own half warp
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(sm.p + (tx + 16 * j) * kPs + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+    __syncthreads();                // K has been read by all
+    store();                        // V
+    __syncthreads();
+    if (t0 + kBN < t.hi) {
+      locate(t0 + kBN);
+      fetch(p.k, p.k_sb, p.k_sh, p.k_st);
+    }
 #pragma unroll 4
     for (int k = 0; k < kBN; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(ps + k * kPs + ty * 4);
+      const float4 a = *reinterpret_cast<const float4*>(sm.p + k * kPs + ty * 4);
 #pragma unroll
       for (int e = 0; e < DV; e += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(vs + k * D + tx * 4 + (e / 4) * 64);
+        const float4 b = *reinterpret_cast<const float4*>(sm.kv + k * LD + tx * 4 + (e / 4) * 64);
         const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
@@ -154,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) fd_prefix_simt_kernel(const __grid_c
         }
       }
     }
+    __syncthreads();                // V and P have been read by all
   }
   if (bad_page) atomicOr(p.flags, FD_DEVFLAG_PAGE);
   pdl_trigger();
@@ -177,11 +208,11 @@ template <class T, int D>
 cudaError_t launch(const PrefixParams& p, cudaStream_t stream) {
   auto kernel = fd_prefix_simt_kernel<T, D>;
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.apply(kernel, (int)smem_bytes<D>());
+  cudaError_t e = opt_in.apply(kernel, (int)sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.S, (unsigned)p.Hkv,
                   (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start ? p.P : 1, kBM));
-  return launch_pdl(kernel, grid, kThreads, smem_bytes<D>(), stream, p);
+  return launch_pdl(kernel, grid, kThreads, sizeof(Smem<D>), stream, p);
 }
 
 }  // namespace
@@ -189,8 +220,7 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t stream) {
 // dtype: that of q and the caches, f32 or bf16.
 cudaError_t launch_prefix_simt(const PrefixParams& p, int32_t dtype, int d, cudaStream_t stream) {
   if (dtype == FD_F32) return d == 128 ? launch<float, 128>(p, stream) : launch<float, 64>(p, stream);
-  return d == 128 ? launch<__nv_bfloat16, 128>(p, stream)
-                  : launch<__nv_bfloat16, 64>(p, stream);
+  return d == 128 ? launch<__nv_bfloat16, 128>(p, stream) : launch<__nv_bfloat16, 64>(p, stream);
 }
 
 }  // namespace fd
