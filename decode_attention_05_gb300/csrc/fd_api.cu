@@ -769,7 +769,8 @@ fd_status run_decode(CacheKind kind, const fd_tensor* q, const fd_tensor* k_cach
                      const int32_t* seq_lens, const fd_tensor* block_table, int32_t page_size,
                      int32_t num_splits, fd_tensor* out, float* lse_out, void* workspace,
                      size_t workspace_bytes, void* stream, const fd_options* options,
-                     bool need_out, int32_t selftest_stall = 0) {
+                     bool need_out, int32_t selftest_stall = 0, fd_status (*before)(void*) = nullptr,
+                     void* before_arg = nullptr) {
   Settings cfg;
   if (!resolve_settings(options, &cfg))
     return fail(FD_ERR_INVALID_ARG, "fd_options holds an unknown path, merge mode or schedule");
@@ -786,6 +787,11 @@ fd_status run_decode(CacheKind kind, const fd_tensor* q, const fd_tensor* k_cach
   if (st != FD_OK) return st;
   pr.p.selftest_stall = selftest_stall;
   const cudaStream_t s = (cudaStream_t)stream;
+  if (before) {
+    st = before(before_arg);
+    if (st != FD_OK) return st;
+    pr.p.late_wait = 1;
+  }
   if (need_out && pr.fused) return launch_partial(pr, s);   // one launch merges in-kernel
   pr.p.counters = nullptr;          // the merge, if any, is a separate kernel
   st = launch_partial(pr, s);
@@ -794,6 +800,18 @@ fd_status run_decode(CacheKind kind, const fd_tensor* q, const fd_tensor* k_cach
 }
 
 }  // namespace
+
+namespace fd {
+fd_status run_partial_behind(const fd_tensor* q, const fd_tensor* k_cache, const fd_tensor* v_cache,
+                             const float* k_scale, const float* v_scale, const int32_t* seq_lens,
+                             const fd_tensor* block_table, int32_t page_size, int32_t num_splits,
+                             void* workspace, size_t workspace_bytes, void* stream,
+                             const fd_options* options, fd_status (*before)(void*), void* arg) {
+  return run_decode(CacheKind::kByDtype, q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
+                    page_size, num_splits, nullptr, nullptr, workspace, workspace_bytes, stream, options,
+                    false, 0, before, arg);
+}
+}  // namespace fd
 
 extern "C" {
 

@@ -121,6 +121,22 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The start of a partial kernel: wait for the previous kernel's memory -- or, with
+// Params::late_wait, only make sure that nothing read from here on comes from an L1 line
+// older than this point (what this pass reads was written before that kernel started).
+__device__ __forceinline__ void pdl_start(const Params& p) {
+  if (p.late_wait) __threadfence();
+  else pdl_wait();
+}
+// Its end, called by every CTA's producer (or by a CTA without work): one CTA holds the grid
+// open until the previous kernel is complete.
+__device__ __forceinline__ void pdl_end(const Params& p) {
+  if (p.late_wait && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+    pdl_trigger();
+    pdl_wait();
+  }
+}
+
 // Base-2 exponential on the SFU (MUFU.EX2).  ex2(-inf) = +0.
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -74,6 +74,11 @@ struct Params {
   // 1: split i covers its range with both ends rounded up to whole tiles (split_range in
   // fd_pipeline.cuh): no tile is loaded by two CTAs (the tcgen05 kernel)
   int32_t tile_owned;
+  // 1: this pass was launched behind a kernel that lets it start at once, having itself waited
+  // for everything before it, and whose results only a later kernel reads (the prompt pass of
+  // fd_decode_shared_prefix): no wait at the start (pdl_start), and one CTA waits before the
+  // grid can end (pdl_end), so that whoever waits for this grid has waited for that kernel too
+  int32_t late_wait;
   // Failure-path self-test only (fd_selftest_stalled_decode; 0 otherwise): n > 0 makes the
   // producer of CTA (0, 0, 0) stop before its tile n - 1 and publish nothing more, as if
   // those copies never arrived, so the CTA's bounded waits run out
@@ -134,6 +139,15 @@ cudaError_t launch_partial_kernel(Kernel kernel, dim3 grid, int threads, size_t 
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
 }
+
+// The partial pass over (k_cache, v_cache) as fd_decode_attention_ex with out NULL runs it,
+// with `before` called once every argument has been accepted: it launches the kernel that this
+// pass then runs next to (Params::late_wait).  If it fails, its status is returned.
+fd_status run_partial_behind(const fd_tensor* q, const fd_tensor* k_cache, const fd_tensor* v_cache,
+                             const float* k_scale, const float* v_scale, const int32_t* seq_lens,
+                             const fd_tensor* block_table, int32_t page_size, int32_t num_splits,
+                             void* workspace, size_t workspace_bytes, void* stream,
+                             const fd_options* options, fd_status (*before)(void*), void* arg);
 
 // Record `message` as the calling thread's fd_last_error() and return `st`.
 fd_status record_error(fd_status st, const char* message);

@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     }
     prefetch_first_tiles<TT>(p, &tk, &tv, kPrefetchTiles, (int)blockIdx.y);
   }
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   const SplitInfo si = split_info<TT>(p);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(
@@ -722,6 +722,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
   if (si.n_tiles == 0) {            // empty split: weight 0 in the merge, nothing to load
     write_empty_split(p, si, threadIdx.x);
     pdl_trigger();
+    pdl_end(p);
     if (p.counters != nullptr && warp < SH::NCW)
       arrive_and_merge<SH::D, SH::NCW>(p, si, threadIdx.x, &ctl->last);
     return;
@@ -742,6 +743,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     prefetch_tensormap(&tv);
     produce_tiles<TT, STAGES>(p, si, &tk, &tv, stages, ctl, lane);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 
@@ -811,7 +813,7 @@ __global__ void __maxnreg__(200)
   constexpr int TT = SH::TT, STAGES = SH::STAGES;
   static_assert(SH::WIDE, "wide shape");
   if (threadIdx.x == SH::NCW * 32) prefetch_first_tiles<TT>(p, &tk, &tv, kPrefetchTiles, (int)blockIdx.y);
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   const SplitInfo si = split_info<TT>(p);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(
@@ -821,6 +823,7 @@ __global__ void __maxnreg__(200)
   if (si.n_tiles == 0) {            // empty split: weight 0 in the merge, nothing to load
     write_empty_split(p, si, threadIdx.x);
     pdl_trigger();
+    pdl_end(p);
     if (p.counters != nullptr && warp < SH::NCW)
       arrive_and_merge<SH::D, SH::NCW>(p, si, threadIdx.x, &ctl->last);
     return;
@@ -841,6 +844,7 @@ __global__ void __maxnreg__(200)
     prefetch_tensormap(&tv);
     produce_tiles<TT, STAGES>(p, si, &tk, &tv, stages, ctl, lane);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 
@@ -906,7 +910,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
         prefetch_first_tiles<TOK>(p, &tk, &tv, kPrefetchHeadTiles, (int)blockIdx.y * kHeadGroup);
     }
   }
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   SplitInfo si = split_info<TOK>(p);
   si.g = blockIdx.y * kHeadGroup;                 // first kv head of the group
   extern __shared__ uint8_t smem_raw[];
@@ -918,6 +922,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     for (int i = threadIdx.x; i < kHeadGroup * p.n_rows; i += blockDim.x)
       put_empty_row<Consumer<SH>::direct_ok()>(p, si.b, si.g + i / p.n_rows, i % p.n_rows, si.split);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 
@@ -936,6 +941,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     prefetch_tensormap(&tv);
     produce_tiles<TOK, STAGES, kHeadGroup>(p, si, &tk, &tv, stages, ctl, lane);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 
@@ -989,7 +995,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
   if constexpr (G <= 8) {
     if (threadIdx.x == SH::NCW * 32) prefetch_first_item<TT, 1>(p, &tk, &tv, kPrefetchTiles);
   }
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1012,6 +1018,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     prefetch_tensormap(&tv);
     produce_items<TT, STAGES, (G <= 8)>(p, &tk, &tv, stages, ctl, lane);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 
@@ -1104,7 +1111,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     if (threadIdx.x == SH::NCW * 32)
       prefetch_first_item<TOK, kHeadGroup>(p, &tk, &tv, kPrefetchHeadTiles);
   }
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1126,6 +1133,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     prefetch_tensormap(&tv);
     produce_items<TOK, STAGES, Consumer<SH>::direct_ok(), kHeadGroup>(p, &tk, &tv, stages, ctl, lane);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 
@@ -1183,7 +1191,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
   constexpr int TT = SH::TT, STAGES = SH::STAGES;
   static_assert(SH::WIDE && SH::PERSIST && SH::G == 8, "wide groups of up to 32 rows");
   if (threadIdx.x == SH::NCW * 32) prefetch_first_item<TT, 1>(p, &tk, &tv, kPrefetchTiles);
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1205,6 +1213,7 @@ __global__ void __launch_bounds__(SH::THREADS, 2)
     prefetch_tensormap(&tv);
     produce_items<TT, STAGES, Consumer<SH>::direct_ok(), 1>(p, &tk, &tv, stages, ctl, lane);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 

@@ -104,7 +104,7 @@ __global__ void __maxnreg__(200)
                            const __grid_constant__ Params p) {
   constexpr int G = SH::G, EPL = SH::EPL, LPR = SH::LPR, RPW = SH::RPW, TT = SH::TT;
   constexpr int STAGES = SH::STAGES;
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   const SplitInfo si = split_info<TT>(p);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(
@@ -114,6 +114,7 @@ __global__ void __maxnreg__(200)
   if (si.n_tiles == 0) {            // empty split: weight 0 in the merge, nothing to load
     write_empty_split(p, si, threadIdx.x);
     pdl_trigger();
+    pdl_end(p);
     if (p.counters != nullptr && warp < SH::NCW)
       arrive_and_merge<SH::D, SH::NCW>(p, si, threadIdx.x, &ctl->last);
     return;
@@ -134,6 +135,7 @@ __global__ void __maxnreg__(200)
     prefetch_tensormap(&tv);
     produce_tiles<TT, STAGES>(p, si, &tk, &tv, stages, ctl, lane);
     pdl_trigger();
+    pdl_end(p);
     return;
   }
 

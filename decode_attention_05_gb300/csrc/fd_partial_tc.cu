@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Contiguous caches only: with 64-token pages the page-id prefetch measured slower on
   // this kernel (97.8 against 95.9 us, 4 query tokens on the 128K GQA workload).
   if (threadIdx.x == 8 * 32) prefetch_first_tiles<kTcTT>(p, &tk, &tv, kTcStages, (int)blockIdx.y);
-  pdl_wait();                       // inputs of this step are visible
+  pdl_start(p);                     // inputs of this step are visible
   const SplitInfo si = split_info<kTcTT>(p);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (si.n_tiles == 0) {            // empty split: weight 0 in the merge, nothing to load
     write_empty_split(p, si, t);
     pdl_trigger();
+    pdl_end(p);
     if (p.counters != nullptr && warp < 8) arrive_and_merge<kTcD, 8>(p, si, t, &ctl->pipe.last);
     return;
   }
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tensormap(&tv);
     produce_tiles_shared<kTcTT, kTcStages>(p, si, &tk, &tv, stages, &ctl->pipe, lane,
                                            p.tail_share != 0);
+    pdl_end(p);
   } else {
     // Set-up of the MMA operands (every warp but the producer): tensor memory, Q and the
     // zeroed P columns.

@@ -53,11 +53,11 @@ __device__ __forceinline__ void group_rows(const PrefixParams& p, int g, int& b0
     b1 = p.B;
     return;
   }
-  const int s0 = g == 0 ? 0 : __ldcg(p.group_start + g);
-  const int s1 = g < p.P ? __ldcg(p.group_start + g + 1) : p.B;
+  const int s0 = g == 0 ? 0 : p.group_start[g];
+  const int s1 = g < p.P ? p.group_start[g + 1] : p.B;
   b0 = min(max(s0, 0), p.B);
   b1 = min(max(s1, b0), p.B);
-  if (b0 != s0 || b1 != s1 || (g == 0 && __ldcg(p.group_start) != 0)) atomicOr(p.flags, FD_DEVFLAG_OFFSETS);
+  if (b0 != s0 || b1 != s1 || (g == 0 && p.group_start[0] != 0)) atomicOr(p.flags, FD_DEVFLAG_OFFSETS);
 }
 
 // The tile that index z names: the groups' tiles in order, and behind them those of the
@@ -98,7 +98,7 @@ __device__ __forceinline__ bool find_tile(const PrefixParams& p, int z, PrefixTi
 // The tile's prompt length and split `s` of it: whole BN-token tiles, evenly shared.
 template <int BN>
 __device__ __forceinline__ void split_of(const PrefixParams& p, int s, PrefixTile& t) {
-  int64_t L = t.group < p.P ? __ldcg(p.prefix_lens + t.group) : 0;
+  int64_t L = t.group < p.P ? p.prefix_lens[t.group] : 0;
   if (L < 0 || L > p.L_cap) {
     if ((threadIdx.x & 31) == 0) atomicOr(p.flags, FD_DEVFLAG_SEQ_LEN);
     L = L < 0 ? 0 : p.L_cap;

@@ -1,7 +1,7 @@
 // fd_prefix_api.cu -- the C ABI of attention over shared prompts (include/fd.h): argument
 // checks, the prompt pass's split count, workspace layout, and the three launches of a call:
-// partials over each row's own cache (the kernels of fd_decode_partial), partials over the
-// shared prompts (fd_prefix.cuh), and the merge of both sets.
+// partials over the shared prompts (fd_prefix.cuh), partials over each row's own cache (the
+// kernels of fd_decode_partial), and the merge of both sets.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -47,16 +47,36 @@ Layout layout(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d, int32_t 
   return w;
 }
 
-// Splits of the rows' own keys: the count of a plain decode call, and more where that call
-// would run head-group tiles (small pages; four kv heads a CTA) on few rows.  A plain call's
-// rows are long then; here the own part is short, and one split of a quarter of the kv heads
-// leaves most SMs without work (32 rows of up to 1024 tokens, 16-token pages: 49 us with one).
-int32_t own_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d, int64_t L_cap, int32_t num_splits) {
+// Splits of the rows' own keys: the count of a plain decode call, except where its kernel
+// leaves SMs without work because it expects long rows.
+//  - Small pages (16 and 32 tokens) run head-group tiles, four kv heads a CTA: two CTAs per SM
+//    of at least 128 tokens (32 rows of up to 1024 tokens, 16-token pages: 49 -> 22 us).
+//  - More than 16 query rows per kv head plan for one CTA per SM: two of at least 64 tokens.
+// small_pages: of the table, or true to ask for the larger count of the two (workspace sizes).
+int32_t own_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d, int64_t L_cap, int32_t num_splits,
+                   bool small_pages) {
   const int32_t s = fd_resolve_num_splits_q(B, Q, Hq, Hkv, d, L_cap, num_splits);
-  if (num_splits > 0 || d != 128 || Hkv % fd::kHeadGroup != 0 || Q * (Hq / Hkv) > fd::kMaxNarrowRows) return s;
-  const int64_t ctas = (int64_t)B * Hkv / fd::kHeadGroup, sms = fd::sm_count();
-  const int64_t want = std::min((2 * sms + ctas - 1) / ctas, (L_cap + 127) / 128);
+  const bool wide = Q * (Hq / Hkv) > fd::kMaxNarrowRows;
+  if (num_splits > 0 || !(wide || (small_pages && d == 128 && Hkv % fd::kHeadGroup == 0))) return s;
+  const int64_t ctas = (int64_t)B * (wide ? Hkv : Hkv / fd::kHeadGroup), sms = fd::sm_count();
+  const int64_t want = wide ? std::min(2 * sms / ctas, (L_cap + 63) / 64)
+                            : std::min((2 * sms + ctas - 1) / ctas, (L_cap + 127) / 128);
   return (int32_t)std::max<int64_t>(s, std::min<int64_t>(want, kMaxSplits));
+}
+
+struct PromptPass {
+  const fd::PrefixParams* p;
+  const CUtensorMap *tk, *tv;       // tk nullptr: CUDA cores
+  int32_t dtype;
+  int d;
+  cudaStream_t stream;
+};
+fd_status launch_prompt_pass(void* arg) {
+  const PromptPass& a = *static_cast<const PromptPass*>(arg);
+  const cudaError_t e =
+      a.tk ? fd::launch_prefix_tc(*a.p, a.dtype == FD_F8E4M3, a.d, *a.tk, *a.tv, a.stream)
+           : fd::launch_prefix_simt(*a.p, a.dtype, a.d, a.stream);
+  return e == cudaSuccess ? FD_OK : fd::record_error(FD_ERR_CUDA, cudaGetErrorString(e));
 }
 
 }  // namespace
@@ -83,7 +103,7 @@ size_t fd_shared_prefix_workspace_size(int32_t B, int32_t Q, int32_t Hq, int32_t
     return 0;
   return layout(B, Q, Hq, Hkv, d,
                 fd_resolve_prefix_splits(B, Q, Hq, Hkv, P, L_prefix_cap, prefix_splits),
-                own_splits(B, Q, Hq, Hkv, d, L_cap, num_splits))
+                own_splits(B, Q, Hq, Hkv, d, L_cap, num_splits, true))
       .total;
 }
 
@@ -182,12 +202,13 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   const int64_t L_cap = block_table ? block_table->shape[1] * page_size : k_cache->shape[2];
   const int32_t Sp = fd_resolve_prefix_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv,
                                               (int32_t)P, Lp, prefix_splits);
-  const int32_t S = own_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv, (int32_t)d, L_cap, num_splits);
+  const int32_t S = own_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv, (int32_t)d, L_cap, num_splits,
+                               block_table && (page_size == 16 || page_size == 32));
   if (((uintptr_t)workspace & (kAlign - 1)) != 0) return bad("workspace must be 256-byte aligned");
   const Layout wl = layout((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv, (int32_t)d, Sp, S);
   if (workspace_bytes < wl.total)
     return fd::record_error(FD_ERR_WORKSPACE_TOO_SMALL, "workspace is smaller than fd_shared_prefix_workspace_size");
-  if (fd::prefix_row_tiles(B, Q * G, group_start ? P : 1, 64) > 65535) return unsupported("grid too large");
+  if (fd::prefix_row_tiles(B, Q * G, group_start ? P : 1, 16) > 65535) return unsupported("grid too large");
 
   fd::PrefixParams p;
   memset(&p, 0, sizeof p);
@@ -226,16 +247,15 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
     if (st != FD_OK) return st;
   }
 
-  // The rows' own keys first: this call checks their arguments and launches nothing if one
-  // is wrong.
-  const fd_status st = fd_decode_attention_ex(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
-                                              block_table ? page_size : 0, S, nullptr, nullptr, workspace,
-                                              wl.own, stream, options);
+  // The rows' own keys: once their arguments are accepted too, the prompt pass is launched (on
+  // error nothing is), and their pass right behind it, to run on the SMs that it leaves free --
+  // it is bound by the tensor cores with many rows, theirs by memory.
+  PromptPass prompt = {&p, tc ? &tk : nullptr, &tv, kd, (int)d, (cudaStream_t)stream};
+  const fd_status st = fd::run_partial_behind(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
+                                              block_table ? page_size : 0, S, workspace, wl.own, stream,
+                                              options, &launch_prompt_pass, &prompt);
   if (st != FD_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = tc ? fd::launch_prefix_tc(p, fp8, (int)d, tk, tv, s)
-                     : fd::launch_prefix_simt(p, kd, (int)d, s);
-  if (e != cudaSuccess) return fd::record_error(FD_ERR_CUDA, cudaGetErrorString(e));
 
   fd::MergeParams mp;
   memset(&mp, 0, sizeof mp);
@@ -250,7 +270,7 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   mp.out_sb = out->stride[0], mp.out_sj = multi ? out->stride[1] : 0, mp.out_sh = out->stride[hd];
   mp.out_bf16 = out->dtype == FD_BF16 ? 1 : 0;
   mp.lse_out = lse_out;
-  e = fd::launch_prefix_merge(mp, s);
+  const cudaError_t e = fd::launch_prefix_merge(mp, s);
   if (e != cudaSuccess) return fd::record_error(FD_ERR_CUDA, cudaGetErrorString(e));
   return FD_OK;
 }

@@ -1,10 +1,10 @@
 // fd_prefix_simt.cu -- attention of many query rows over a shared prompt, on CUDA cores
 // (fd_prefix.cuh says what the pass computes): f32 inputs, and bf16 as a cross-check.
 //
-// A CTA holds 64 query rows of one group and kv head and walks its split of the prompt in
+// A CTA holds 64 query rows (16 for groups of at most that many) of one group and kv head and walks its split of the prompt in
 // tiles of 64 tokens: S = Q K^T, the running maximum and sum of the softmax ("AI Infra: math
 // and infra optimisation in large models", section 2.6), O = O 2^(m_old - m_new) + P V.  All
-// in f32.  256 threads: thread (ty, tx) of a 16 x 16 grid has the scores of rows 4 ty .. + 3
+// in f32.  256 threads: thread (ty, tx) of a 16 x 16 grid has the scores of rows 4 ty .. + 3 (row ty)
 // and tokens tx + 16 j (j < 4), and the outputs of the same rows and D / 16 dims, so a row's 16
 // threads lie in one half warp and reduce with shuffles.
 //
@@ -19,15 +19,14 @@
 namespace fd {
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kThreads = 256;
-constexpr int kPs = kBM + 4;        // padded leading dimension of P
+constexpr int kBN = 64, kThreads = 256;
 
-template <int D>
+template <int D, int BM>
 struct Smem {
-  static constexpr int LD = D + 4;
-  float q[kBM * LD];
+  static constexpr int LD = D + 4, LP = BM + 4;   // padded leading dimensions of q, k, v and p
+  float q[BM * LD];
   float kv[kBN * LD];               // the tile's K, then its V
-  float p[kBN * kPs];
+  float p[kBN * LP];
   float mask[kBN];                  // 0, or -inf for a token without weight
   PrefixTile tile;
   int found;
@@ -39,20 +38,22 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* a) {
   return make_float4(bf16lo_to_f32(r.x), bf16hi_to_f32(r.x), bf16lo_to_f32(r.y), bf16hi_to_f32(r.y));
 }
 
-template <class T, int D>
+template <class T, int D, int BM>
 __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __grid_constant__ PrefixParams p) {
-  using SM = Smem<D>;
-  constexpr int LD = SM::LD, DV = D / 16;
+  using SM = Smem<D, BM>;
+  constexpr int LD = SM::LD, kPs = SM::LP, DV = D / 16;
+  constexpr int R = BM / 16;                   // query rows of a thread: 4 or 1
   constexpr int RPT = kThreads / (D / 4);      // tile rows that the threads load at once
   constexpr int NR = kBN / RPT;                // ... and how often
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
   pdl_wait();
+  pdl_trigger();                    // the pass over the rows' own keys runs next to this one
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int split = blockIdx.x, g = blockIdx.y;
   if (tid < 32) {
     PrefixTile t;
-    const bool ok = find_tile<kBM>(p, (int)blockIdx.z, t);
+    const bool ok = find_tile<BM>(p, (int)blockIdx.z, t);
     if (ok) split_of<kBN>(p, split, t);
     if (tid == 0) {
       sm.tile = t;
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __gri
     return;
   }
   const int lr = tid / (D / 4), lc = tid % (D / 4) * 4;   // this thread's row and dims of a load
-  for (int r = lr; r < kBM; r += RPT) {
+  for (int r = lr; r < BM; r += RPT) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < t.rows) x = load4(static_cast<const T*>(p.q) + prefix_q_offset(p, t, g, r) + lc);
     const float f = p.scale_log2;
@@ -106,9 +107,9 @@ __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __gri
     for (int i = 0; i < NR; ++i) *reinterpret_cast<float4*>(sm.kv + (lr + i * RPT) * LD + lc) = next[i];
   };
 
-  float m[4], l[4], acc[4][DV];
+  float m[R], l[R], acc[R][DV];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
     m[i] = kNegInf;
     l[i] = 0.f;
 #pragma unroll
@@ -124,15 +125,15 @@ __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __gri
     }
     __syncthreads();
     fetch(p.v, p.v_sb, p.v_sh, p.v_st);
-    float s[4][4] = {};
+    float s[R][4] = {};
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
       float4 b[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sm.kv + (tx + 16 * j) * LD + k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 a = *reinterpret_cast<const float4*>(sm.q + (ty * 4 + i) * LD + k);
+      for (int i = 0; i < R; ++i) {
+        const float4 a = *reinterpret_cast<const float4*>(sm.q + (ty * R + i) * LD + k);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           s[i][j] = fmaf(a.x, b[j].x, fmaf(a.y, b[j].y, fmaf(a.z, b[j].z, fmaf(a.w, b[j].w, s[i][j]))));
@@ -142,10 +143,10 @@ __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __gri
     for (int j = 0; j < 4; ++j) {
       const bool out = sm.mask[tx + 16 * j] != 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i][j] = out ? kNegInf : s[i][j];
+      for (int i = 0; i < R; ++i) s[i][j] = out ? kNegInf : s[i][j];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       float mt = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
@@ -159,8 +160,11 @@ __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __gri
       m[i] = mn;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(sm.p + (tx + 16 * j) * kPs + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+    for (int j = 0; j < 4; ++j) {
+      float* dst = sm.p + (tx + 16 * j) * kPs + ty * R;
+      if constexpr (R == 4) *reinterpret_cast<float4*>(dst) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+      else *dst = s[0][j];
+    }
     __syncthreads();                // K has been read by all
     store();                        // V
     __syncthreads();
@@ -170,29 +174,32 @@ __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __gri
     }
 #pragma unroll 4
     for (int k = 0; k < kBN; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(sm.p + k * kPs + ty * 4);
+      float a[R];
+      if constexpr (R == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(sm.p + k * kPs + ty * 4);
+        a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
+      } else {
+        a[0] = sm.p[k * kPs + ty];
+      }
 #pragma unroll
       for (int e = 0; e < DV; e += 4) {
         const float4 b = *reinterpret_cast<const float4*>(sm.kv + k * LD + tx * 4 + (e / 4) * 64);
         const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          acc[0][e + f] = fmaf(a.x, bb[f], acc[0][e + f]);
-          acc[1][e + f] = fmaf(a.y, bb[f], acc[1][e + f]);
-          acc[2][e + f] = fmaf(a.z, bb[f], acc[2][e + f]);
-          acc[3][e + f] = fmaf(a.w, bb[f], acc[3][e + f]);
+#pragma unroll
+          for (int i = 0; i < R; ++i) acc[i][e + f] = fmaf(a[i], bb[f], acc[i][e + f]);
         }
       }
     }
     __syncthreads();                // V and P have been read by all
   }
   if (bad_page) atomicOr(p.flags, FD_DEVFLAG_PAGE);
-  pdl_trigger();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-    const int r = ty * 4 + i;
+    const int r = ty * R + i;
     if (r >= t.rows) continue;
     const int64_t at = prefix_flat_row(p, t, g, r) * p.S + split;
     if (tx == 0) p.lse_part[at] = l[i] == 0.f ? kNegInf : (m[i] + __log2f(l[i])) * 0.6931471805599453f;
@@ -204,23 +211,31 @@ __global__ void __launch_bounds__(kThreads, 2) fd_prefix_simt_kernel(const __gri
   }
 }
 
-template <class T, int D>
+template <class T, int D, int BM>
 cudaError_t launch(const PrefixParams& p, cudaStream_t stream) {
-  auto kernel = fd_prefix_simt_kernel<T, D>;
+  auto kernel = fd_prefix_simt_kernel<T, D, BM>;
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.apply(kernel, (int)sizeof(Smem<D>));
+  cudaError_t e = opt_in.apply(kernel, (int)sizeof(Smem<D, BM>));
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.S, (unsigned)p.Hkv,
-                  (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start ? p.P : 1, kBM));
-  return launch_pdl(kernel, grid, kThreads, sizeof(Smem<D>), stream, p);
+                  (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start ? p.P : 1, BM));
+  return launch_pdl(kernel, grid, kThreads, sizeof(Smem<D, BM>), stream, p);
+}
+
+// 16-row tiles where groups of equal size would not have more: such a call is bound by its
+// reads of K and V, and 64-row tiles would do four times the arithmetic on padding.
+template <class T, int D>
+cudaError_t launch_rows(const PrefixParams& p, cudaStream_t stream) {
+  const int64_t rows = ((int64_t)p.B + p.P - 1) / p.P * p.Q * p.G;
+  return rows <= 16 ? launch<T, D, 16>(p, stream) : launch<T, D, 64>(p, stream);
 }
 
 }  // namespace
 
 // dtype: that of q and the caches, f32 or bf16.
 cudaError_t launch_prefix_simt(const PrefixParams& p, int32_t dtype, int d, cudaStream_t stream) {
-  if (dtype == FD_F32) return d == 128 ? launch<float, 128>(p, stream) : launch<float, 64>(p, stream);
-  return d == 128 ? launch<__nv_bfloat16, 128>(p, stream) : launch<__nv_bfloat16, 64>(p, stream);
+  if (dtype == FD_F32) return d == 128 ? launch_rows<float, 128>(p, stream) : launch_rows<float, 64>(p, stream);
+  return d == 128 ? launch_rows<__nv_bfloat16, 128>(p, stream) : launch_rows<__nv_bfloat16, 64>(p, stream);
 }
 
 }  // namespace fd

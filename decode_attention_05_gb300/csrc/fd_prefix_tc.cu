@@ -180,7 +180,7 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
     if (paged) {                    // lane j: page j of the tile
       const int64_t pi = (t0 >> p.log2_page) + lane;
       id = -2;
-      if (lane < boxes && pi < used) id = __ldcg(p.table + (int64_t)t.group * p.table_sb + pi);
+      if (lane < boxes && pi < used) id = p.table[(int64_t)t.group * p.table_sb + pi];
       const bool wrong = lane < boxes && pi < used && (id < 0 || id >= p.num_pages);
       const uint32_t bad = __ballot_sync(0xffffffffu, wrong);
       if (bad != 0 && lane == 0) atomicOr(p.flags, FD_DEVFLAG_PAGE);
@@ -568,9 +568,8 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
     tc_alloc(smem_addr(&ctl->tmem), kCols);
     tc_relinquish();
   }
-  // No wait for the previous kernel here: it is the pass over the rows' own keys, which lets
-  // this one start only once it has itself waited for everything before it, and whose results
-  // only the merge reads.  (Inputs are read through L2, where earlier kernels' writes are.)
+  pdl_wait();
+  pdl_trigger();                    // the pass over the rows' own keys runs next to this one
   if (warp == 8) {
     prefetch_tensormap(&tk);
     prefetch_tensormap(&tv);
@@ -614,8 +613,8 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       const int w = warp >> 2, r = tid & 127;
       // A scale of K multiplies the scores (its sign q, since the running maximum is taken
       // before the factor; a factor of 0 becomes one that only keeps -inf what it is).
-      const float ks = p.k_scale != nullptr ? __ldcg(p.k_scale + g) : 1.f;
-      const float vs = p.v_scale != nullptr ? __ldcg(p.v_scale + g) : 1.f;
+      const float ks = p.k_scale != nullptr ? p.k_scale[g] : 1.f;
+      const float vs = p.v_scale != nullptr ? p.v_scale[g] : 1.f;
       const float sl2 = SH::FP8 ? fmaxf(p.scale_log2 * fabsf(ks), 1e-37f) : p.scale_log2;
       // Q to shared memory, [64-dim slab][row][128 B] with 16-byte groups XORed by the row.
       // Two row tiles: a thread its row; one: the two threads of a row half of it each.
@@ -628,7 +627,7 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
         const int c0 = two_rows ? 0 : w * (D / 16), c1 = two_rows ? D / 8 : c0 + D / 16;
 #pragma unroll 4
         for (int c = c0; c < c1; ++c) {
-          uint4 x = live ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
+          uint4 x = live ? src[c] : make_uint4(0, 0, 0, 0);
           if constexpr (SH::FP8) {            // q as f16
             uint32_t* y = &x.x;
 #pragma unroll
@@ -644,7 +643,6 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       named_bar_sync(2, 320);
       float m, l;
       if (!softmax<SH>(p, t, n_tiles, two_rows, w, r, sl2, base, ctl, m, l) && lane == 0) set_abort(p, ctl);
-      pdl_trigger();
       named_bar_sync(1, 256);                 // both streams are done, or one gave up
       float2* stats = reinterpret_cast<float2*>(base);        // Q is not needed any more
       stats[w * kRows + r] = make_float2(m, l);
@@ -664,7 +662,6 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
   } else if (found) {               // nothing of the prompt in this split
     if (tid < t.rows) p.lse_part[prefix_flat_row(p, t, g, tid) * p.S + split] = kNegInf;
   }
-  pdl_wait();                       // this grid ends after that pass: the merge waits for both
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
