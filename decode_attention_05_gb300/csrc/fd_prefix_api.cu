@@ -60,7 +60,7 @@ int32_t own_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d, int
   if (num_splits > 0 || !(wide || (small_pages && d == 128 && Hkv % fd::kHeadGroup == 0))) return s;
   const int64_t ctas = (int64_t)B * (wide ? Hkv : Hkv / fd::kHeadGroup), sms = fd::sm_count();
   const int64_t want = wide ? std::min(2 * sms / ctas, (L_cap + 63) / 64)
-                            : std::min((2 * sms + ctas - 1) / ctas, (L_cap + 127) / 128);
+                            : std::min(2 * sms / ctas, (L_cap + 127) / 128);
   return (int32_t)std::max<int64_t>(s, std::min<int64_t>(want, kMaxSplits));
 }
 

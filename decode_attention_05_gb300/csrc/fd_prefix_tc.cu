@@ -33,8 +33,8 @@
 // [64-dim slab][token][128 B], 128-byte swizzle.  A page of fewer than 128 tokens is loaded
 // slab by slab, so that a tile has the same layout whatever the page size.
 //
-// FP8 caches: TMA fills a ring of code tiles (16 KB), and another warpgroup widens them to
-// f16 (exactly: E4M3 fits f16) into the operand ring, so the products are those of f16 q, K, P
+// FP8 caches: TMA fills a ring of code tiles (16 KB), and two more warpgroups widen them, one
+// the K and one the V tiles, to f16 (exactly: E4M3 fits f16) into the operand ring, so the products are those of f16 q, K, P
 // and V.  (8-bit products would need q and P in 8 bits.)  A kv head's scale of K multiplies
 // the scores, its scale of V the output.
 #include <cuda_fp16.h>
@@ -54,8 +54,10 @@ template <int D_, bool FP8_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr bool FP8 = FP8_;
-  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int THREADS = FP8 ? 640 : 384;
   static constexpr uint32_t TYPE = FP8 ? 0u : 1u;               // operands f16 or bf16
+  // Weights (16-bit pairs) formed between stores: fewer where five warpgroups share the registers.
+  static constexpr int CH = FP8 ? 16 : 32;
   static constexpr int SLABS = D / 64;
   static constexpr uint32_t SLAB_BYTES = kTok * 128;            // 64 dims of 128 tokens
   static constexpr uint32_t TILE_BYTES = SLABS * SLAB_BYTES;
@@ -217,19 +219,19 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
   }
 }
 
-// ---------------------------------------------------------------- widening (FP8, a warpgroup)
-// Thread r widens token row r of every tile: 16 codes of one 16-byte group become two groups
+// ---------------------------------------------------------------- widening (FP8, two warpgroups)
+// Warpgroup kv widens the K (0) or V (1) tiles, thread r token row r of each: 16 codes of one 16-byte group become two groups
 // of f16.  A quarter warp's eight rows hit eight different bank groups in both layouts.  Rows
 // of tokens without weight become zeros.
 template <class SH>
 __device__ void widen(const PrefixParams& p, const PrefixTile& t, int n_tiles, int raw_stages, uint8_t* base,
-                      Ctl* ctl, int r) {
+                      Ctl* ctl, int kv, int r) {
   const int lane = r & 31;
   const bool pages = p.table != nullptr && p.page_size < kTok;
   bool ok = true;
-  int rs = 0, round = 0;
-  for (int e = 0; e < 2 * n_tiles; ++e) {
-    const int n = e >> 1, st = e % SH::STAGES;
+  int rs = kv, round = 0;
+  for (int n = 0; n < n_tiles; ++n) {
+    const int e = 2 * n + kv, st = e % SH::STAGES;
     ok = warp_wait(ctl, smem_addr(&ctl->raw_full[rs]), round & 1);
     if (ok && e >= SH::STAGES) ok = warp_wait(ctl, smem_addr(&ctl->empty[st]), ((e / SH::STAGES) - 1) & 1);
     if (!ok) break;
@@ -238,7 +240,7 @@ __device__ void widen(const PrefixParams& p, const PrefixTile& t, int n_tiles, i
     const bool live = tok < t.hi && !((bad >> (pages ? r >> p.log2_page : 0)) & 1u);
     const uint8_t* src = base + SH::raw_offset(rs) + r * 128;
     uint8_t* dst = base + SH::RING_OFF + st * SH::TILE_BYTES + r * 128;
-#pragma unroll
+#pragma unroll 4
     for (int c = 0; c < 8; ++c) {
       const uint4 x = live ? *reinterpret_cast<const uint4*>(src + ((c ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -261,7 +263,8 @@ __device__ void widen(const PrefixParams& p, const PrefixTile& t, int n_tiles, i
       mbar_arrive(smem_addr(&ctl->raw_empty[rs]));
       mbar_arrive(smem_addr(&ctl->full[st]));
     }
-    if (++rs == raw_stages) rs = 0, ++round;
+    rs += 2;
+    if (rs >= raw_stages) rs -= raw_stages, ++round;
   }
   if (!ok && lane == 0) set_abort(p, ctl);
 }
@@ -368,11 +371,11 @@ __device__ __forceinline__ void issue(const PrefixParams& p, int w, int n_tiles_
 }
 
 // ---------------------------------------------------------------- softmax (a warpgroup a stream)
-// The weights 2^(s sl2 - base) of 64 scores as pairs of 16-bit operands, added to `sum`.
+// The weights 2^(s sl2 - base) of 2 CH scores as pairs of 16-bit operands, added to `sum`.
 template <class SH>
 __device__ __forceinline__ void weights(const float* s, uint64_t scale2, uint64_t off2, uint32_t* pk, uint64_t* sum) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
+  for (int j = 0; j < SH::CH; ++j) {
     float a, b;
     unpair(fma2(pair(s[2 * j], s[2 * j + 1]), scale2, off2), a, b);
     a = ex2(a);
@@ -433,7 +436,7 @@ __device__ __forceinline__ bool softmax(const PrefixParams& p, const PrefixTile&
     const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
     // A row without a key so far takes this tile's maximum (there is nothing to rescale).
     float base = m == kNegInf ? (mt == kNegInf ? 0.f : mt) : m;
-    uint32_t pk[32];
+    uint32_t pk[SH::CH];
     uint64_t sum[2] = {0ull, 0ull};
     weights<SH>(s, scale2, pair(-base, -base), pk, sum);
     const bool grows = m != kNegInf && mt > m + 8.f;
@@ -444,23 +447,26 @@ __device__ __forceinline__ bool softmax(const PrefixParams& p, const PrefixTile&
       l *= c;
       if (grows) base = m = mt;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        float o[32];
-        tc_ld32(oc + q * 32, o);
+      for (int q = 0; q < D / 16; ++q) {      // few columns at a time: S waits in registers
+        float o[16];
+        tc_ld16(oc + q * 16, o);
+        uint32_t x[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] *= c;
-        tc_st32(oc + q * 32, o);
+        for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(o[j] * c);
+        tc_st16(oc + q * 16, x);
       }
       sum[0] = sum[1] = 0ull;
       weights<SH>(s, scale2, pair(-base, -base), pk, sum);
     }
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half == 1) weights<SH>(s + 64, scale2, pair(-base, -base), pk, sum);
-      tc_st32w(sc + half * 32, pk);
+    for (int c = 0; c < kTok / 2 / SH::CH; ++c) {
+      if (c > 0) weights<SH>(s + c * 2 * SH::CH, scale2, pair(-base, -base), pk, sum);
+      if constexpr (SH::CH == 32) tc_st32w(sc + c * SH::CH, pk);
+      else tc_st16(sc + c * SH::CH, pk);
+      if ((c + 1) * SH::CH % 32 != 0) continue;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&ctl->p_half[w][half]));
+      if (lane == 0) mbar_arrive(smem_addr(&ctl->p_half[w][(c + 1) * SH::CH / 32 - 1]));
     }
     float a, b;
     unpair(add2(sum[0], sum[1]), a, b);
@@ -591,15 +597,15 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
   const int raw_stages = two_rows ? 2 : 4;
 
   if (n_tiles > 0) {
-    // Registers of the warpgroups (softmax, softmax, producer and issuers, widening): 216 +
-    // 216 + 72 is what three were launched with (168 each), 184 + 184 + 56 + 88 four (128).
+    // Registers of the warpgroups (softmax twice, producer and issuers, widening twice): 2 x 216
+    // + 72 is what three were launched with (168 each), 2 x 168 + 48 + 2 x 48 five (96).
     if (warp >= 12) {
       if constexpr (SH::FP8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        widen<SH>(p, t, n_tiles, raw_stages, base, ctl, tid & 127);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        widen<SH>(p, t, n_tiles, raw_stages, base, ctl, (warp - 12) >> 2, tid & 127);
       }
     } else if (warp >= 8) {
-      if constexpr (SH::FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if constexpr (SH::FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
       else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp == 8) {
         produce<SH>(p, t, g, n_tiles, raw_stages, two_rows, &tk, &tv, smem_addr(base), ctl, lane);
@@ -608,7 +614,7 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
         issue<SH>(p, warp - 9, n_tiles, two_rows, smem_addr(base), ctl);
       }
     } else {
-      if constexpr (SH::FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      if constexpr (SH::FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
       else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       const int w = warp >> 2, r = tid & 127;
       // A scale of K multiplies the scores (its sign q, since the running maximum is taken
