@@ -148,6 +148,8 @@ def _declare(L):
     L.fd_decode_shared_prefix.restype = ctypes.c_int
     L.fd_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32,
                                           i32, i32, vp, vp, vp, sz, vp, O]
+    L.fd_selftest_stalled_shared_prefix.restype = ctypes.c_int
+    L.fd_selftest_stalled_shared_prefix.argtypes = [*L.fd_decode_shared_prefix.argtypes, i32]
     L.fd_shared_prefix_workspace_size.restype = sz
     L.fd_shared_prefix_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i64, i64, i32, i32]
     L.fd_resolve_prefix_splits.restype = i32
@@ -615,10 +617,11 @@ def decode_attention_shared_prefix(
         k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
         prefix_splits: int = 0, num_splits: int = 0, out: Optional[torch.Tensor] = None,
         lse_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-        out_dtype=None, stream=None, options: Optional[FdOptions] = None
-        ) -> Tuple[torch.Tensor, torch.Tensor]:
+        out_dtype=None, stream=None, options: Optional[FdOptions] = None,
+        selftest_stall: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """fd_decode_shared_prefix: attention over each row's group's prompt and its own cache;
-    returns (out, lse_out).  Missing buffers are allocated with torch."""
+    returns (out, lse_out).  Missing buffers are allocated with torch.  (``selftest_stall``:
+    fd_selftest_stalled_shared_prefix with that copy, for the failure-path tests.)"""
     if q.dim() == 4:
         B, Qn, Hq, d = q.shape
     else:
@@ -645,13 +648,17 @@ def decode_attention_shared_prefix(
     place = _launch_place(stream, q, k_prefix, v_prefix, prefix_lens, group_start, prefix_table,
                           k_cache, v_cache, seq_lens, block_table, k_scale, v_scale, out, lse_out,
                           workspace)
-    status = lib().fd_decode_shared_prefix(
+    args = (
         _packed(q), _packed(k_prefix), _packed(v_prefix), _ints(prefix_lens, "prefix_lens"),
         _ints(group_start, "group_start"), _packed(prefix_table), _packed(k_cache),
         _packed(v_cache), _floats(k_scale, "k_scale"), _floats(v_scale, "v_scale"),
         _ints(seq_lens, "seq_lens"), _packed(block_table), page_size, prefix_splits, num_splits,
         _packed(out), lse_out.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), place, _ref(options))
+    if selftest_stall is None:
+        status = lib().fd_decode_shared_prefix(*args)
+    else:
+        status = lib().fd_selftest_stalled_shared_prefix(*args, selftest_stall)
     if status != FD_OK:
         _check(status)
     return out, lse_out

@@ -34,6 +34,7 @@ struct PrefixParams {
   float* o_part;                    // [B, Q, Hq, S, d]
   uint32_t* flags;
   float scale_log2;                 // log2(e) / sqrt(d)
+  int32_t selftest_stall;           // n > 0: CTA (0, 0, 0)'s producer stops before its copy n - 1
   const float *k_scale, *v_scale;   // FP8: per kv head, or nullptr = 1
 };
 

@@ -107,16 +107,19 @@ size_t fd_shared_prefix_workspace_size(int32_t B, int32_t Q, int32_t Hq, int32_t
       .total;
 }
 
-fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
-                                  const fd_tensor* v_prefix, const int32_t* prefix_lens,
-                                  const int32_t* group_start, const fd_tensor* prefix_table,
-                                  const fd_tensor* k_cache, const fd_tensor* v_cache,
-                                  const float* k_scale, const float* v_scale,
-                                  const int32_t* seq_lens, const fd_tensor* block_table,
-                                  int32_t page_size, int32_t prefix_splits, int32_t num_splits,
-                                  fd_tensor* out, float* lse_out, void* workspace,
-                                  size_t workspace_bytes, void* stream,
-                                  const fd_options* options) {
+}  // extern "C"
+
+// A call; stall > 0: fd_selftest_stalled_shared_prefix.
+static fd_status run_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
+                                   const fd_tensor* v_prefix, const int32_t* prefix_lens,
+                                   const int32_t* group_start, const fd_tensor* prefix_table,
+                                   const fd_tensor* k_cache, const fd_tensor* v_cache,
+                                   const float* k_scale, const float* v_scale,
+                                   const int32_t* seq_lens, const fd_tensor* block_table,
+                                   int32_t page_size, int32_t prefix_splits, int32_t num_splits,
+                                   fd_tensor* out, float* lse_out, void* workspace,
+                                   size_t workspace_bytes, void* stream, const fd_options* options,
+                                   int32_t stall) {
   if (!q || !k_prefix || !v_prefix || !k_cache || !v_cache || !out)
     return bad("q, k_prefix, v_prefix, k_cache, v_cache and out are required");
   if (!q->data || !k_prefix->data || !v_prefix->data || !k_cache->data || !v_cache->data || !out->data)
@@ -163,6 +166,7 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   for (int i = 0; i + 1 < q->ndim; ++i) {
     if ((q->stride[i] * esize(q->dtype)) % 16) return bad("q strides must be multiples of 16 bytes");
     if ((out->stride[i] * esize(out->dtype)) % 16) return bad("out strides must be multiples of 16 bytes");
+    if (out->stride[i] <= 0 && out->shape[i] > 1) return bad("out strides must be positive");
   }
   for (int i = 0; i < 3; ++i)
     if (k_prefix->stride[i] <= 0 || v_prefix->stride[i] <= 0 || (k_prefix->stride[i] * es) % 16 ||
@@ -232,6 +236,7 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   p.o_part = reinterpret_cast<float*>(ws + wl.o_off);
   p.flags = reinterpret_cast<uint32_t*>(ws);
   p.scale_log2 = (float)(1.4426950408889634 / __builtin_sqrt((double)d));
+  p.selftest_stall = stall;
   p.k_scale = fp8 ? k_scale : nullptr;
   p.v_scale = fp8 ? v_scale : nullptr;
 
@@ -273,6 +278,38 @@ fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
   const cudaError_t e = fd::launch_prefix_merge(mp, s);
   if (e != cudaSuccess) return fd::record_error(FD_ERR_CUDA, cudaGetErrorString(e));
   return FD_OK;
+}
+
+extern "C" {
+
+fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix,
+                                  const fd_tensor* v_prefix, const int32_t* prefix_lens,
+                                  const int32_t* group_start, const fd_tensor* prefix_table,
+                                  const fd_tensor* k_cache, const fd_tensor* v_cache,
+                                  const float* k_scale, const float* v_scale,
+                                  const int32_t* seq_lens, const fd_tensor* block_table,
+                                  int32_t page_size, int32_t prefix_splits, int32_t num_splits,
+                                  fd_tensor* out, float* lse_out, void* workspace,
+                                  size_t workspace_bytes, void* stream,
+                                  const fd_options* options) {
+  return run_shared_prefix(q, k_prefix, v_prefix, prefix_lens, group_start, prefix_table, k_cache,
+                           v_cache, k_scale, v_scale, seq_lens, block_table, page_size,
+                           prefix_splits, num_splits, out, lse_out, workspace, workspace_bytes,
+                           stream, options, 0);
+}
+
+fd_status fd_selftest_stalled_shared_prefix(
+    const fd_tensor* q, const fd_tensor* k_prefix, const fd_tensor* v_prefix,
+    const int32_t* prefix_lens, const int32_t* group_start, const fd_tensor* prefix_table,
+    const fd_tensor* k_cache, const fd_tensor* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* seq_lens, const fd_tensor* block_table, int32_t page_size, int32_t prefix_splits,
+    int32_t num_splits, fd_tensor* out, float* lse_out, void* workspace, size_t workspace_bytes,
+    void* stream, const fd_options* options, int32_t stall_copy) {
+  if (stall_copy < 0) return bad("stall_copy must be >= 0");
+  return run_shared_prefix(q, k_prefix, v_prefix, prefix_lens, group_start, prefix_table, k_cache,
+                           v_cache, k_scale, v_scale, seq_lens, block_table, page_size,
+                           prefix_splits, num_splits, out, lse_out, workspace, workspace_bytes,
+                           stream, options, stall_copy + 1);
 }
 
 }  // extern "C"

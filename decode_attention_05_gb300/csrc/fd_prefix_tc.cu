@@ -173,6 +173,9 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
   const int stages = SH::FP8 ? raw_stages : SH::stages(two_rows);
   uint64_t* fulls = SH::FP8 ? ctl->raw_full : ctl->full;
   uint64_t* empties = SH::FP8 ? ctl->raw_empty : ctl->empty;
+  auto drain = [&](int n) {         // let the copies in flight land before the CTA ends
+    for (int i = max(0, n - stages); i < n; ++i) mbar_wait(smem_addr(&fulls[i % stages]), (i / stages) & 1);
+  };
   int issued = 0, st = 0, round = 0;          // entry, its stage, and how often the ring wrapped
   bool ok = true;
   for (int n = 0; n < n_tiles && ok; ++n) {
@@ -195,6 +198,9 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
     __syncwarp();
     for (int kv = 0; kv < 2; ++kv) {
       const uint32_t full = smem_addr(&fulls[st]);
+      if (p.selftest_stall > 0 && issued == p.selftest_stall - 1 && blockIdx.x == 0 && blockIdx.y == 0 &&
+          blockIdx.z == 0)
+        return drain(issued);       // as if the next copies never arrived: the others' waits run out
       if (round > 0) ok = warp_wait(ctl, smem_addr(&empties[st]), (round - 1) & 1);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(full, SH::FP8 ? SH::RAW_BYTES : SH::TILE_BYTES);
@@ -212,10 +218,9 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
       if (++st == stages) st = 0, ++round;
     }
   }
-  if (!ok) {                        // let the copies in flight land before the CTA ends
+  if (!ok) {
     if (lane == 0) set_abort(p, ctl);
-    for (int i = max(0, issued - stages); i < issued; ++i)
-      mbar_wait(smem_addr(&fulls[i % stages]), (i / stages) & 1);
+    drain(issued);
   }
 }
 

@@ -557,6 +557,20 @@ FD_API fd_status fd_decode_shared_prefix(const fd_tensor* q, const fd_tensor* k_
                                          fd_tensor* out, float* lse_out, void* workspace,
                                          size_t workspace_bytes, void* stream,
                                          const fd_options* options);
+/* Self-test of the prompt pass's failure path: the call, except that the copy producer of one
+ * CTA stops before its copy `stall_copy` (0-based; copies alternate between K and V tiles), as
+ * if those copies never arrived.  That CTA's bounded waits give up after ~2 s, raise
+ * FD_DEVFLAG_TIMEOUT, wait for products and copies in flight, and write an empty split; the
+ * outputs of its rows are wrong, the context and workspace stay usable.  stall_copy >= 0; a
+ * stall past the CTA's last copy changes nothing.  bf16 and FP8 caches (the CUDA-core pass has
+ * no copies to wait for).  Not for production use. */
+FD_API fd_status fd_selftest_stalled_shared_prefix(
+    const fd_tensor* q, const fd_tensor* k_prefix, const fd_tensor* v_prefix,
+    const int32_t* prefix_lens, const int32_t* group_start, const fd_tensor* prefix_table,
+    const fd_tensor* k_cache, const fd_tensor* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* seq_lens, const fd_tensor* block_table, int32_t page_size, int32_t prefix_splits,
+    int32_t num_splits, fd_tensor* out, float* lse_out, void* workspace, size_t workspace_bytes,
+    void* stream, const fd_options* options, int32_t stall_copy);
 /* Bytes of workspace such a call needs (0 for invalid sizes): P prompts of capacity
  * L_prefix_cap, own caches of capacity L_cap.  Depends on the current device's SM count
  * where a split count is 0. */

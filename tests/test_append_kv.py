@@ -333,6 +333,17 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
+def test_tensors_elsewhere_are_refused():
+    for name in ("q", "k_cache", "seq_lens"):
+        a = {k: (x.cuda() if isinstance(x, torch.Tensor) else x) for k, x in _cpu_case().items()}
+        a[name] = a[name].cpu()
+        with pytest.raises(ValueError):
+            fd.append_kv(**a)
+    with pytest.raises(ValueError):
+        fd.append_kv(**_cpu_case())
+
+
+@pytest.mark.gpu
 def test_other_stream_and_graph():
     d, ws = 128, torch.zeros(256, dtype=torch.uint8, device="cuda")
     k = torch.randn(4, 2, d, device="cuda").to(BF)

@@ -71,6 +71,7 @@ REFUSED = [
     ("prefix page size", dict(page_size=12, prefix_table=torch.zeros(1, 4, dtype=torch.int32)), INVALID),
     ("prefix pool's page", dict(page_size=16, prefix_table=torch.zeros(1, 4, dtype=torch.int32)), INVALID),
     ("prefix table dtype", dict(page_size=64, prefix_table=torch.zeros(1, 4)), INVALID),
+    ("overlapping out rows", dict(out=_bf(1, 8, 128).expand(4, 8, 128)), INVALID),
     ("misaligned workspace", dict(workspace=_aligned(1 << 20)[16:]), INVALID),
     ("prefix splits", dict(prefix_splits=-1), INVALID),
     ("splits", dict(num_splits=4097), INVALID),
@@ -389,6 +390,93 @@ def test_device_flags():
     d.plens = [44, 40]
     for options in (None, fd.options(path=fd.FD_PATH_SIMT)):
         d.check(*_run(c, flags=fd.FD_DEVFLAG_PAGE, prefix_table=table, options=options))
+
+
+@gpu
+@pytest.mark.parametrize("cache", [BF, F8])
+@pytest.mark.parametrize("rows,stall", [(3, 0), (3, 1), (3, 4), (90, 0), (90, 5)])
+def test_stalled_copies_end_with_a_flag(cache, rows, stall):
+    """Copies that never arrive: the waits run out, the call ends with a flag, rows that the
+    stalled CTA (row tile 0, kv head 0, split 0) does not serve are right, and the same workspace
+    then gives right results."""
+    c = Case(cache=cache, groups=((rows, 900),), own=(5, 40), seed=17)
+    a = c.args()
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    out, lse = fd.decode_attention_shared_prefix(workspace=ws, selftest_stall=stall, prefix_splits=1, **a)
+    assert fd.read_device_error(ws) == fd.FD_DEVFLAG_TIMEOUT
+    got = fd.decode_attention_shared_prefix(workspace=ws, prefix_splits=1, **a)
+    assert fd.read_device_error(ws) == 0
+    c.check(*got)
+    assert torch.equal(out[:, 4:], got[0][:, 4:]) and torch.equal(lse[:, 4:], got[1][:, 4:])
+
+
+@gpu
+def test_stall_past_the_last_copy_changes_nothing():
+    c = Case(groups=((3, 300),), own=(5, 40), seed=18)
+    a = c.args()
+    want = _run(c)
+    got = _run(c, selftest_stall=1000)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
+def test_two_threads_on_one_stream():
+    """Two threads' calls, interleaved launch by launch on one stream, each with its own buffers."""
+    import threading
+    cases = [Case(groups=((3, 300),), own=(5, 40), seed=19),
+             Case(cache=F8, groups=((70, 500), (2, 90)), own=(5, 40), seed=20)]
+    args = [c.args() for c in cases]
+    want = [_run(c) for c in cases]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        got = [fd.decode_attention_shared_prefix(workspace=ws, stream=stream, **args[i]) for _ in range(40)]
+        stream.synchronize()
+        if not all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for o, l in got):
+            wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not wrong
+
+
+@gpu
+def test_inputs_written_just_before_the_call():
+    """Queries, lengths, own keys and prompts rewritten on the stream right before each call."""
+    c = Case(groups=((20, 700), (30, 300)), own=(5, 40, 300), page=16, seed=21)
+    a = c.args()
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    want = fd.decode_attention_shared_prefix(workspace=ws, **a)
+    names = ("q", "k_prefix", "v_prefix", "k_cache", "v_cache", "seq_lens", "prefix_lens",
+             "group_start", "prefix_table", "block_table")
+    kept = {n: a[n].clone() for n in names}
+    for _ in range(30):
+        for n in ("q", "k_cache", "v_cache", "k_prefix", "v_prefix"):
+            a[n].fill_(3.0)
+        a["seq_lens"].fill_(1)
+        a["prefix_lens"].fill_(1)
+        fd.decode_attention_shared_prefix(workspace=ws, **a)
+        for n in names:
+            a[n].copy_(kept[n])
+        got = fd.decode_attention_shared_prefix(workspace=ws, **a)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
+def test_tensors_elsewhere_are_refused():
+    c = Case(groups=((3, 30),), own=(5,), seed=22)
+    for name in ("q", "prefix_lens", "k_cache", "seq_lens"):
+        a = c.args()
+        a[name] = a[name].cpu()
+        with pytest.raises(ValueError):
+            fd.decode_attention_shared_prefix(**a)
 
 
 @gpu
