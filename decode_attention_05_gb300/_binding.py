@@ -505,12 +505,12 @@ def _packed(t: Optional[torch.Tensor]) -> Optional[bytes]:
         return None
     shape = t.shape
     n = len(shape)
-    if not 1 <= n <= 4:
-        raise ValueError("fd_tensor holds 1 to 4 dims")
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None:
-        raise TypeError("unsupported dtype %s" % t.dtype)
-    return _LAYOUT[n](t.data_ptr(), dtype, n, *shape, *t.stride())
+    try:
+        return _LAYOUT[n](t.data_ptr(), _DTYPES[t.dtype], n, *shape, *t.stride())
+    except KeyError:
+        raise TypeError("unsupported dtype %s" % t.dtype) from None
+    except (IndexError, TypeError):
+        raise ValueError("fd_tensor holds 1 to 4 dims") from None
 
 
 def _ints(t: Optional[torch.Tensor], name: str) -> Optional[int]:
@@ -528,6 +528,12 @@ def _floats(t: Optional[torch.Tensor], name: str) -> Optional[int]:
     if t.dtype != torch.float32 or not t.is_contiguous():
         raise TypeError("%s must be a contiguous float32 tensor" % name)
     return t.data_ptr()
+
+
+def _check_scales(k_scale, v_scale, k_cache):
+    for s in (k_scale, v_scale):
+        if s is not None and s.numel() != k_cache.shape[1]:
+            raise ValueError("scales need one entry per kv head")
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -573,14 +579,13 @@ def append_kv(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     only through ``workspace`` (see ``read_device_error``)."""
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    B = (k_cache if block_table is None else block_table).shape[0]
+    B = len(k_cache if block_table is None else block_table)
     if seq_lens.numel() != B or (pos_offset is not None and pos_offset.numel() != B):
         raise ValueError("seq_lens and pos_offset need one entry per batch row")
     if cu_tokens is not None and cu_tokens.numel() != B + 1:
         raise ValueError("cu_tokens needs B + 1 entries")
-    for s in (k_scale, v_scale):
-        if s is not None and s.numel() != k_cache.shape[1]:
-            raise ValueError("scales need one entry per kv head")
+    if k_scale is not None or v_scale is not None:
+        _check_scales(k_scale, v_scale, k_cache)
     if workspace is not None and workspace.numel() * workspace.element_size() < 256:
         raise ValueError("the workspace's header needs 256 bytes")
     place = _launch_place(stream, k, v, q, q_out, k_cache, v_cache, seq_lens, cos_sin, pos_offset,
@@ -631,9 +636,8 @@ def decode_attention_shared_prefix(
         raise ValueError("need one length per batch row and per prefix")
     if group_start is not None and group_start.numel() != P + 1:
         raise ValueError("group_start needs P + 1 entries")
-    for s in (k_scale, v_scale):
-        if s is not None and s.numel() != k_cache.shape[1]:
-            raise ValueError("scales need one entry per kv head")
+    if k_scale is not None or v_scale is not None:
+        _check_scales(k_scale, v_scale, k_cache)
     if out is None:
         out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
     if lse_out is None:

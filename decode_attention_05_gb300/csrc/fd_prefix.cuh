@@ -20,6 +20,8 @@ namespace fd {
 
 struct PrefixParams {
   int32_t B, Q, Hq, Hkv, G, P;
+  int32_t log2_g;                   // G is a power of two
+  uint32_t per_row_inv;             // ceil(2^32 / (Q G)), 0 for Q G = 1: see prefix_row
   const void* q;                    // [B, Q, Hq, d]
   int64_t q_sb, q_sj, q_sh;
   const void *k, *v;                // [P, Hkv, L_cap, d] or pages [num_pages, Hkv, page, d]
@@ -68,6 +70,13 @@ template <int BM>
 __device__ __forceinline__ bool find_tile(const PrefixParams& p, int z, PrefixTile& t) {
   const int lane = threadIdx.x & 31;
   const int per_row = p.Q * p.G;
+  if (p.group_start == nullptr) {             // one group: no search
+    t.group = 0;
+    t.b0 = 0;
+    t.row0 = z * BM;
+    t.rows = min(BM, p.B * per_row - t.row0);
+    return t.rows > 0;
+  }
   int before = 0;
   for (int g0 = 0; g0 <= p.P; g0 += 32) {
     const int g = g0 + lane;
@@ -110,18 +119,27 @@ __device__ __forceinline__ void split_of(const PrefixParams& p, int s, PrefixTil
   t.hi = min(tiles * (s + 1) / p.S * BN, L);
 }
 
-// Query row r of a tile: its batch row, and its flat index over [B, Q, Hq].
-__device__ __forceinline__ int64_t prefix_flat_row(const PrefixParams& p, const PrefixTile& t, int g,
-                                                   int r) {
-  const int per_row = p.Q * p.G;
-  const int x = t.row0 + r, i = x / per_row, y = x - i * per_row, j = y / p.G, h = y - j * p.G;
-  return ((int64_t)(t.b0 + i) * p.Q + j) * p.Hq + (int64_t)g * p.G + h;
+// Query row r of a tile: its batch row b, query token j and head g G + h.  A row's place x in
+// its group is divided by Q G as floor(x inv / 2^32), inv = ceil(2^32 / (Q G)): exact as long as
+// x (Q G - 1) < 2^32, and x < 65536 * 64, Q G <= 64.
+__device__ __forceinline__ void prefix_row(const PrefixParams& p, const PrefixTile& t, int r, int& b, int& j, int& h) {
+  const int x = t.row0 + r;
+  const int i = p.per_row_inv ? (int)__umulhi((unsigned)x, p.per_row_inv) : x;
+  const int y = x - i * p.Q * p.G;
+  b = t.b0 + i;
+  j = y >> p.log2_g;
+  h = y & (p.G - 1);
 }
-__device__ __forceinline__ int64_t prefix_q_offset(const PrefixParams& p, const PrefixTile& t, int g,
-                                                   int r) {
-  const int per_row = p.Q * p.G;
-  const int x = t.row0 + r, i = x / per_row, y = x - i * per_row, j = y / p.G, h = y - j * p.G;
-  return (int64_t)(t.b0 + i) * p.q_sb + (int64_t)j * p.q_sj + ((int64_t)g * p.G + h) * p.q_sh;
+// Its flat index over [B, Q, Hq], and where its query starts.
+__device__ __forceinline__ int64_t prefix_flat_row(const PrefixParams& p, const PrefixTile& t, int g, int r) {
+  int b, j, h;
+  prefix_row(p, t, r, b, j, h);
+  return ((int64_t)b * p.Q + j) * p.Hq + (int64_t)g * p.G + h;
+}
+__device__ __forceinline__ int64_t prefix_q_offset(const PrefixParams& p, const PrefixTile& t, int g, int r) {
+  int b, j, h;
+  prefix_row(p, t, r, b, j, h);
+  return (int64_t)b * p.q_sb + (int64_t)j * p.q_sj + ((int64_t)g * p.G + h) * p.q_sh;
 }
 
 // The merge of a row's partials: those of its prompt (set 0) and of its own keys (set 1).

@@ -217,6 +217,8 @@ static fd_status run_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix
   fd::PrefixParams p;
   memset(&p, 0, sizeof p);
   p.B = (int32_t)B, p.Q = (int32_t)Q, p.Hq = (int32_t)Hq, p.Hkv = (int32_t)Hkv, p.G = (int32_t)G, p.P = (int32_t)P;
+  while ((1 << p.log2_g) < p.G) ++p.log2_g;
+  p.per_row_inv = Q * G > 1 ? (uint32_t)(((uint64_t{1} << 32) + Q * G - 1) / (Q * G)) : 0;
   p.q = q->data;
   p.q_sb = q->stride[0], p.q_sj = multi ? q->stride[1] : 0, p.q_sh = q->stride[hd];
   p.k = k_prefix->data, p.v = v_prefix->data;

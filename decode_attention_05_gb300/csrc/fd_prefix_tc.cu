@@ -49,6 +49,7 @@ namespace {
 constexpr int kRows = 128, kTok = 128;
 constexpr uint32_t kCols = 512, kOCol = 256;
 constexpr int kMaxStages = 9;
+constexpr int kPad = 4;              // floats behind each row of the results' scratch
 
 template <int D_, bool FP8_>
 struct Shape {
@@ -99,6 +100,10 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<Shape<128, false>>() <= 227 * 1024 && smem_bytes<Shape<64, false>>() <= 227 * 1024 &&
                   smem_bytes<Shape<128, true>>() <= 227 * 1024,
               "one CTA per SM");
+static_assert(2 * kRows * (128 + kPad) * 4 <= 5 * Shape<128, false>::TILE_BYTES &&
+                  2 * kRows * (64 + kPad) * 4 <= 8 * Shape<64, false>::TILE_BYTES &&
+                  2 * kRows * (128 + kPad) * 4 <= Shape<128, true>::CTL_OFF - Shape<128, true>::RING_OFF,
+              "the results' scratch lies in the drained ring");
 
 __device__ __forceinline__ bool aborted(Ctl* c) {
   return *reinterpret_cast<volatile int32_t*>(&c->abort) != 0;
@@ -151,11 +156,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ void store8(float* a, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "f"(v[0]),
-               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
 }
 
 // ---------------------------------------------------------------- TMA producer (one warp)
@@ -414,9 +414,10 @@ __device__ __forceinline__ bool softmax(const PrefixParams& p, const PrefixTile&
     const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[n & 7]);
     if (left < kTok || bad != 0u) { // past the prompt's end, or on an invalid page: no weight
 #pragma unroll
-      for (int j = 0; j < kTok; ++j) {
-        const bool out = j >= left || ((bad >> (pages ? j >> log2_page : 0)) & 1u);
-        s[j] = out ? kNegInf : s[j];
+      for (int j = 0; j < kTok; ++j) s[j] = j >= left ? kNegInf : s[j];
+      if (bad != 0u) {
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) s[j] = (bad >> (pages ? j >> log2_page : 0)) & 1u ? kNegInf : s[j];
       }
       if constexpr (!SH::FP8) {     // (widen() has cleared them)
         // Their V rows may hold anything, and 0 * NaN would reach O: clear them.
@@ -488,35 +489,51 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? kNegInf : (m + __log2f(l)) * 0.6931471805599453f;   // NaN stays NaN
 }
 
-// Two row tiles: a thread writes its row.
+// A warp's 32 rows of COLS f32 (lane = row, `at` its row of o_part or -1) to memory by way of
+// shared memory: written from the lanes' registers directly, every store would touch 32 lines
+// (128 KB a CTA took 7000 cycles).  Rows are padded by 16 bytes against bank conflicts.
+template <int D, int COLS>
+__device__ __forceinline__ void store_rows(float* o_part, int64_t at, int col, float* scratch, int lane) {
+  constexpr int LD = COLS + kPad, PER = COLS / 4;     // lanes that hold one row
+  __syncwarp();
+#pragma unroll 8
+  for (int i = 0; i < 32; i += 32 / PER) {
+    const int r = i + lane / PER, c = lane % PER * 4;
+    const int64_t to = __shfl_sync(0xffffffffu, at, r);
+    const float4 x = *reinterpret_cast<const float4*>(scratch + r * LD + c);
+    if (to >= 0) *reinterpret_cast<float4*>(o_part + to * D + col + c) = x;
+  }
+}
+
+// Two row tiles: a thread's row is row r of stream w.
 template <int D>
 __device__ void write_rows(const PrefixParams& p, const PrefixTile& t, int g, int split, int w, int r, float m,
-                           float l, float vscale) {
+                           float l, float vscale, float* ring) {
   const uint32_t oc = ((uint32_t)(r & ~31) << 16) + kOCol + w * D;
   const bool mine = w * kRows + r < t.rows;
   const int64_t at = mine ? prefix_flat_row(p, t, g, w * kRows + r) * p.S + split : 0;
+  float* scratch = ring + (size_t)(w * kRows + (r & ~31)) * (D + kPad);
   const float f = vscale / l;
-#pragma unroll
+#pragma unroll 1                    // (code that runs once is fetched while it runs: keep it short)
   for (int q = 0; q < D / 32; ++q) {
     float o[32];
-    __syncwarp();
     tc_ld32(oc + q * 32, o);
-    if (mine && l != 0.f) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] *= f;
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) store8(p.o_part + at * D + q * 32 + j, o + j);
-    }
+    for (int j = 0; j < 32; j += 4)
+      *reinterpret_cast<float4*>(scratch + (r & 31) * (D + kPad) + q * 32 + j) =
+          make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
   }
   if (mine) p.lse_part[at] = lse_of(m, l);
+  store_rows<D, D>(p.o_part, mine && l != 0.f ? at : -1, 0, scratch, r & 31);
 }
 
 // Two streams of the same rows: merge them (M = max m, c = 2^(m - M), O = sum c O / sum c l).
 // Both streams' O of a row lie in its TMEM lane: either thread of the row forms half the dims.
 template <int D>
 __device__ void merge_rows(const PrefixParams& p, const PrefixTile& t, int g, int split, int n_tiles, int half,
-                           int r, const float (&m)[2], const float (&l)[2], float vscale) {
-  const uint32_t oc = ((uint32_t)(r & ~31) << 16) + kOCol + half * (D / 2);
+                           int r, const float (&m)[2], const float (&l)[2], float vscale, float* ring) {
+  constexpr int N = D / 2;
+  const uint32_t oc = ((uint32_t)(r & ~31) << 16) + kOCol + half * N;
   const float M = fmaxf(m[0], m[1]);
   float c[2];
 #pragma unroll
@@ -524,26 +541,28 @@ __device__ void merge_rows(const PrefixParams& p, const PrefixTile& t, int g, in
   const float L = l[0] * c[0] + l[1] * c[1], f = vscale / L;
   const bool mine = r < t.rows;
   const int64_t at = mine ? prefix_flat_row(p, t, g, r) * p.S + split : 0;
-#pragma unroll
-  for (int q = 0; q < D / 64; ++q) {
+  float* scratch = ring + (size_t)(half * kRows + (r & ~31)) * (N + kPad);
+#pragma unroll 1
+  for (int q = 0; q < N / 32; ++q) {
     float o[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) o[j] = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < 2; ++w) {
       if (w >= n_tiles) continue;             // a split of one tile has no second stream
+      const float cw = w ? c[1] : c[0];
       float x[32];
-      __syncwarp();
       tc_ld32(oc + w * D + q * 32, x);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = c[w] != 0.f ? fmaf(x[j], c[w] * f, o[j]) : o[j];
+      for (int j = 0; j < 32; ++j) o[j] = cw != 0.f ? fmaf(x[j], cw * f, o[j]) : o[j];
     }
-    if (mine && L != 0.f) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) store8(p.o_part + at * D + half * (D / 2) + q * 32 + j, o + j);
-    }
+    for (int j = 0; j < 32; j += 4)
+      *reinterpret_cast<float4*>(scratch + (r & 31) * (N + kPad) + q * 32 + j) =
+          make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
   }
   if (mine && half == 0) p.lse_part[at] = lse_of(M, L);
+  store_rows<D, N>(p.o_part, mine && L != 0.f ? at : -1, half * N, scratch, r & 31);
 }
 
 template <class SH>
@@ -627,27 +646,32 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       const float ks = p.k_scale != nullptr ? p.k_scale[g] : 1.f;
       const float vs = p.v_scale != nullptr ? p.v_scale[g] : 1.f;
       const float sl2 = SH::FP8 ? fmaxf(p.scale_log2 * fabsf(ks), 1e-37f) : p.scale_log2;
-      // Q to shared memory, [64-dim slab][row][128 B] with 16-byte groups XORed by the row.
-      // Two row tiles: a thread its row; one: the two threads of a row half of it each.
+      // Q to shared memory, [64-dim slab][row][128 B] with 16-byte groups XORed by the row.  A
+      // warp has 32 rows (16, of a single row tile): each lane finds where one of them starts,
+      // then LPR lanes read a whole row, eight loads of a thread in flight.
       {
-        const int row = two_rows ? w * kRows + r : r;
-        const bool live = row < t.rows;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                          (live ? prefix_q_offset(p, t, g, row) : 0));
-        uint8_t* dst = base + (two_rows ? w * SH::TILE_BYTES : 0u) + r * 128;
-        const int c0 = two_rows ? 0 : w * (D / 16), c1 = two_rows ? D / 8 : c0 + D / 16;
-#pragma unroll 4
-        for (int c = c0; c < c1; ++c) {
-          uint4 x = live ? src[c] : make_uint4(0, 0, 0, 0);
-          if constexpr (SH::FP8) {            // q as f16
-            uint32_t* y = &x.x;
+        constexpr int LPR = D / 8, AT_ONCE = 8;
+        const int rows = two_rows ? 32 : 16, row0 = warp * rows, c = lane % LPR;
+        const int64_t mine = prefix_q_offset(p, t, g, min(row0 + lane, t.rows - 1));
+        const uint4* q = static_cast<const uint4*>(p.q) + c;
+        const float f = ks < 0.f ? -1.f : 1.f;
+        uint8_t* dst = base + (row0 / kRows) * SH::TILE_BYTES + (c >> 3) * SH::SLAB_BYTES;
+#pragma unroll 1
+        for (int r0 = lane / LPR; r0 < rows; r0 += AT_ONCE * (32 / LPR)) {
+          uint4 x[AT_ONCE];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float f = ks < 0.f ? -1.f : 1.f;
-              y[i] = pack_f16(bf16lo_to_f32(y[i]) * f, bf16hi_to_f32(y[i]) * f);
+          for (int k = 0; k < AT_ONCE; ++k) x[k] = q[__shfl_sync(0xffffffffu, mine, r0 + k * (32 / LPR)) >> 3];
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) {
+            const int i = r0 + k * (32 / LPR), row = row0 + i;
+            if (row >= t.rows) x[k] = make_uint4(0, 0, 0, 0);
+            if constexpr (SH::FP8) {          // q as f16
+              uint32_t* y = &x[k].x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_to_f32(y[e]) * f, bf16hi_to_f32(y[e]) * f);
             }
+            if (i < rows) *reinterpret_cast<uint4*>(dst + (row % kRows) * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[k];
           }
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * SH::SLAB_BYTES + (((c & 7) ^ (r & 7)) << 4)) = x;
         }
       }
       fence_proxy_async_smem();
@@ -663,11 +687,11 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
         if (row < t.rows && (two_rows || w == 0))
           p.lse_part[prefix_flat_row(p, t, g, row) * p.S + split] = kNegInf;
       } else if (two_rows) {
-        write_rows<D>(p, t, g, split, w, r, m, l, vs);
+        write_rows<D>(p, t, g, split, w, r, m, l, vs, reinterpret_cast<float*>(base + SH::RING_OFF));
       } else {
         const float2 a = stats[r], b = stats[kRows + r];
         const float ms[2] = {a.x, b.x}, ls[2] = {a.y, b.y};
-        merge_rows<D>(p, t, g, split, n_tiles, w, r, ms, ls, vs);
+        merge_rows<D>(p, t, g, split, n_tiles, w, r, ms, ls, vs, reinterpret_cast<float*>(base + SH::RING_OFF));
       }
     }
   } else if (found) {               // nothing of the prompt in this split
