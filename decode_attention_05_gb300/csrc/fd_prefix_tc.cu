@@ -398,8 +398,6 @@ __device__ __forceinline__ bool softmax(const PrefixParams& p, const PrefixTile&
   const int lane = r & 31;
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
   const uint32_t sc = lanes + w * kTok, oc = lanes + kOCol + w * D;
-  const int log2_page = p.log2_page;
-  const bool pages = p.table != nullptr && p.page_size < kTok;
   const int step = two_rows ? 1 : 2;
   const uint64_t scale2 = pair(sl2, sl2);
   m = kNegInf;
@@ -413,17 +411,18 @@ __device__ __forceinline__ bool softmax(const PrefixParams& p, const PrefixTile&
     tc_ld32x2(sc + 64, sc + 96, s + 64);
     const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[n & 7]);
     if (left < kTok || bad != 0u) { // past the prompt's end, or on an invalid page: no weight
+      const int log2_page = p.page_size > 0 && p.page_size < kTok ? p.log2_page : 7;
 #pragma unroll
       for (int j = 0; j < kTok; ++j) s[j] = j >= left ? kNegInf : s[j];
       if (bad != 0u) {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) s[j] = (bad >> (pages ? j >> log2_page : 0)) & 1u ? kNegInf : s[j];
+        for (int j = 0; j < kTok; ++j) s[j] = (bad >> (j >> log2_page)) & 1u ? kNegInf : s[j];
       }
       if constexpr (!SH::FP8) {     // (widen() has cleared them)
         // Their V rows may hold anything, and 0 * NaN would reach O: clear them.
         const int e = 2 * n + 1, stages = SH::stages(two_rows);
         if (!warp_wait(ctl, smem_addr(&ctl->full[e % stages]), (e / stages) & 1)) return false;
-        if (r >= left || ((bad >> (pages ? r >> log2_page : 0)) & 1u)) {
+        if (r >= left || ((bad >> (r >> log2_page)) & 1u)) {
           uint8_t* v = data + SH::ring_off(two_rows) + (size_t)(e % stages) * SH::TILE_BYTES + r * 128;
 #pragma unroll
           for (int c = 0; c < SH::SLABS * 8; ++c)
@@ -644,7 +643,6 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       // A scale of K multiplies the scores (its sign q, since the running maximum is taken
       // before the factor; a factor of 0 becomes one that only keeps -inf what it is).
       const float ks = p.k_scale != nullptr ? p.k_scale[g] : 1.f;
-      const float vs = p.v_scale != nullptr ? p.v_scale[g] : 1.f;
       const float sl2 = SH::FP8 ? fmaxf(p.scale_log2 * fabsf(ks), 1e-37f) : p.scale_log2;
       // Q to shared memory, [64-dim slab][row][128 B] with 16-byte groups XORed by the row.  A
       // warp has 32 rows (16, of a single row tile): each lane finds where one of them starts,
@@ -682,16 +680,20 @@ __global__ void __launch_bounds__(SH::THREADS, 1)
       float2* stats = reinterpret_cast<float2*>(base);        // Q is not needed any more
       stats[w * kRows + r] = make_float2(m, l);
       named_bar_sync(1, 256);
+      // Read again rather than kept through the loop, whose registers are all in use.
+      const PrefixTile done = ctl->tile;
+      const float vs = p.v_scale != nullptr ? p.v_scale[g] : 1.f;
+      float* scratch = reinterpret_cast<float*>(base + SH::RING_OFF);
       if (aborted(ctl)) {
-        const int row = two_rows ? w * kRows + r : r;
-        if (row < t.rows && (two_rows || w == 0))
-          p.lse_part[prefix_flat_row(p, t, g, row) * p.S + split] = kNegInf;
-      } else if (two_rows) {
-        write_rows<D>(p, t, g, split, w, r, m, l, vs, reinterpret_cast<float*>(base + SH::RING_OFF));
+        const int row = done.rows > kRows ? w * kRows + r : r;
+        if (row < done.rows && (done.rows > kRows || w == 0))
+          p.lse_part[prefix_flat_row(p, done, g, row) * p.S + split] = kNegInf;
+      } else if (done.rows > kRows) {
+        write_rows<D>(p, done, g, split, w, r, m, l, vs, scratch);
       } else {
         const float2 a = stats[r], b = stats[kRows + r];
         const float ms[2] = {a.x, b.x}, ls[2] = {a.y, b.y};
-        merge_rows<D>(p, t, g, split, n_tiles, w, r, ms, ls, vs, reinterpret_cast<float*>(base + SH::RING_OFF));
+        merge_rows<D>(p, done, g, split, n_tiles, w, r, ms, ls, vs, scratch);
       }
     }
   } else if (found) {               // nothing of the prompt in this split
