@@ -12,10 +12,10 @@
 namespace fd {
 namespace {
 
-constexpr int kWarps = 4, kBatch = 8;
+constexpr int kWarps = 4, kBatch = 4;
 
 // W warps fold the partials of one row (W = 4: one row a CTA; 1: four rows a CTA); a lane
-// holds D / 32 dims.  kBatch partials' loads are in flight at once.
+// holds D / 32 dims.
 template <int D, int W>
 __global__ void __launch_bounds__(kWarps * 32) fd_prefix_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int VEC = D / 32;
@@ -25,50 +25,55 @@ __global__ void __launch_bounds__(kWarps * 32) fd_prefix_merge_kernel(const __gr
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * kWarps + warp : (int64_t)blockIdx.x;
+  const int row = W == 1 ? (int)blockIdx.x * kWarps + warp : (int)blockIdx.x;
   if (row >= p.rows) return;
-  const int total = p.S[0] + p.S[1];
   float M = kNegInf, sum = 0.f, acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  for (int s0 = W == 1 ? 0 : warp; s0 < total; s0 += W * kBatch) {
-    float ls[kBatch], v[kBatch][VEC];
+#pragma unroll 1
+  for (int set = 0; set < 2; ++set) {
+    // Pointers that step from batch to batch, so that a partial costs no address arithmetic:
+    // with thousands of rows the instructions, not the bytes, set this kernel's time.
+    int left = p.S[set] - (W == 1 ? 0 : warp);
+    const int64_t first = (int64_t)row * p.S[set] + (W == 1 ? 0 : warp);
+    const float* lse = p.lse[set] + first;
+    const float* o = p.o[set] + first * D + lane * VEC;
+#pragma unroll 1
+    for (; left > 0; left -= W * kBatch, lse += W * kBatch, o += W * kBatch * D) {
+      float ls[kBatch], v[kBatch][VEC];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int s = s0 + W * u;
-      const int set = s < p.S[0] ? 0 : 1;
-      const int64_t at = row * p.S[set] + (set ? s - p.S[0] : s);
-      const bool in = s < total;
-      ls[u] = in ? p.lse[set][at] * kLog2e : kNegInf;
+      for (int u = 0; u < kBatch; ++u) {
+        const bool in = W * u < left;
+        ls[u] = in ? lse[W * u] * kLog2e : kNegInf;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[u][e] = 0.f;
-      if (in) {
-        const float* o = p.o[set] + at * D + lane * VEC;
-        if constexpr (VEC == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(o);
-          v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(o);
-          v[u][0] = x.x, v[u][1] = x.y;
+        for (int e = 0; e < VEC; ++e) v[u][e] = 0.f;
+        if (in) {
+          if constexpr (VEC == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(o + W * u * D);
+            v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(o + W * u * D);
+            v[u][0] = x.x, v[u][1] = x.y;
+          }
         }
       }
+      float mn = M;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, ls[u]);
+      const float c = M == kNegInf ? 0.f : ex2(M - mn);
+      sum *= c;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] *= c;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const bool live = ls[u] != kNegInf;    // a NaN counts: it is the row's result
+        const float w = live ? ex2(ls[u] - mn) : 0.f;
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(w, live ? v[u][e] : 0.f, acc[e]);
+      }
+      M = mn;
     }
-    float mn = M;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, ls[u]);
-    const float c = M == kNegInf ? 0.f : ex2(M - mn);
-    sum *= c;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] *= c;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const bool live = ls[u] != kNegInf;      // a NaN counts: it is the row's result
-      const float w = live ? ex2(ls[u] - mn) : 0.f;
-      sum += w;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(w, live ? v[u][e] : 0.f, acc[e]);
-    }
-    M = mn;
   }
   if constexpr (W > 1) {                       // the warps' states, by the same rule
 #pragma unroll
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(kWarps * 32) fd_prefix_merge_kernel(const __gr
   }
   const bool none = sum == 0.f;                // no key at all
   const float inv = none ? 0.f : 1.f / sum;
-  const int64_t bj = row / p.Hq, b = bj / p.Q;
+  const int bj = row / p.Hq, b = bj / p.Q;
   const int64_t at = b * p.out_sb + (bj - b * p.Q) * p.out_sj + (row - bj * p.Hq) * p.out_sh + lane * VEC;
   if (p.out_bf16) {
     __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at);
