@@ -154,11 +154,11 @@ struct MergeParams {
   float* lse_out;                   // [rows] or nullptr
 };
 
-// Tiles of BM query rows that a call can have at most: each non-empty group (and the rows
-// behind the last) may end in a tile of its own.
-inline int64_t prefix_row_tiles(int64_t B, int64_t per_row, int64_t groups, int64_t BM) {
-  if (groups == 1) return (B * per_row + BM - 1) / BM;
-  const int64_t parts = groups + 1 < B ? groups + 1 : B;
+// Tiles of BM query rows that a call can have at most: with group_start each non-empty group,
+// and the rows behind the last (one group may have some too), may end in a tile of its own.
+inline int64_t prefix_row_tiles(int64_t B, int64_t per_row, bool grouped, int64_t P, int64_t BM) {
+  if (!grouped) return (B * per_row + BM - 1) / BM;
+  const int64_t parts = P + 1 < B ? P + 1 : B;
   return B * per_row / BM + parts;
 }
 

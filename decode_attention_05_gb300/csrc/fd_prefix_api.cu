@@ -64,6 +64,25 @@ int32_t own_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d, int
   return (int32_t)std::max<int64_t>(s, std::min<int64_t>(want, kMaxSplits));
 }
 
+// Splits of the prompts: those of (row tile, kv head) pairs of groups of equal size fill one
+// wave of CTAs.
+int32_t prompt_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t P, int64_t L_cap,
+                      int32_t prefix_splits, int row_tile, int ctas_per_sm, int64_t min_tokens) {
+  if (!sizes_ok(B, Q, Hq, Hkv, 1, P, L_cap, prefix_splits)) return 1;
+  if (prefix_splits > 0) return prefix_splits;
+  const int64_t per = ((int64_t)(B + P - 1) / P) * Q * (Hq / Hkv);
+  const int64_t units = (int64_t)Hkv * std::min<int64_t>(P, B) * ((per + row_tile - 1) / row_tile);
+  const int64_t s = std::min<int64_t>((int64_t)ctas_per_sm * fd::sm_count() / units,
+                                      (L_cap + min_tokens - 1) / min_tokens);
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplits));
+}
+// Of the CUDA-core pass: 64-row tiles, two CTAs per SM, no split below two of its 64-token
+// tiles (its tiles are slow, so a split of 256 tokens is a long chain: 33 rows on 2049 tokens,
+// f32, 43 -> 35 us).
+int32_t simt_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t P, int64_t L_cap, int32_t prefix_splits) {
+  return prompt_splits(B, Q, Hq, Hkv, P, L_cap, prefix_splits, 64, 2, 128);
+}
+
 struct PromptPass {
   const fd::PrefixParams* p;
   const CUtensorMap *tk, *tv;       // tk nullptr: CUDA cores
@@ -85,14 +104,7 @@ extern "C" {
 
 int32_t fd_resolve_prefix_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t P,
                                  int64_t L_cap, int32_t prefix_splits) {
-  if (!sizes_ok(B, Q, Hq, Hkv, 1, P, L_cap, prefix_splits)) return 1;
-  if (prefix_splits > 0) return prefix_splits;
-  const int sms = fd::sm_count();
-  // (row tile, kv head) pairs of groups of equal size; their splits fill one wave of CTAs.
-  const int64_t per = ((int64_t)(B + P - 1) / P) * Q * (Hq / Hkv);
-  const int64_t units = (int64_t)Hkv * std::min<int64_t>(P, B) * ((per + kRowTile - 1) / kRowTile);
-  const int64_t s = std::min<int64_t>(sms / units, (L_cap + kMinSplitTokens - 1) / kMinSplitTokens);
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplits));
+  return prompt_splits(B, Q, Hq, Hkv, P, L_cap, prefix_splits, kRowTile, 1, kMinSplitTokens);
 }
 
 size_t fd_shared_prefix_workspace_size(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t d,
@@ -101,8 +113,10 @@ size_t fd_shared_prefix_workspace_size(int32_t B, int32_t Q, int32_t Hq, int32_t
   if (!sizes_ok(B, Q, Hq, Hkv, d, P, L_prefix_cap, prefix_splits) || L_cap <= 0 || num_splits < 0 ||
       num_splits > kMaxSplits)
     return 0;
+  // The larger of the two passes' counts: the sizes do not say which will run.
   return layout(B, Q, Hq, Hkv, d,
-                fd_resolve_prefix_splits(B, Q, Hq, Hkv, P, L_prefix_cap, prefix_splits),
+                std::max(fd_resolve_prefix_splits(B, Q, Hq, Hkv, P, L_prefix_cap, prefix_splits),
+                         simt_splits(B, Q, Hq, Hkv, P, L_prefix_cap, prefix_splits)),
                 own_splits(B, Q, Hq, Hkv, d, L_cap, num_splits, true))
       .total;
 }
@@ -204,15 +218,18 @@ static fd_status run_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix
   if ((block_table ? block_table->shape[0] : k_cache->shape[0]) != B)
     return bad("k_cache or block_table has another batch size than q");
   const int64_t L_cap = block_table ? block_table->shape[1] * page_size : k_cache->shape[2];
-  const int32_t Sp = fd_resolve_prefix_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv,
-                                              (int32_t)P, Lp, prefix_splits);
+  // ---- the prompt pass: tensor cores for bf16 and FP8, CUDA cores for f32 or when asked for
+  // (with FP8 that is refused with the rows' own keys below)
+  const bool tc = kd != FD_F32 && path != FD_PATH_SIMT;
+  const int32_t Sp = (tc ? fd_resolve_prefix_splits : simt_splits)((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv,
+                                                                   (int32_t)P, Lp, prefix_splits);
   const int32_t S = own_splits((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv, (int32_t)d, L_cap, num_splits,
                                block_table && (page_size == 16 || page_size == 32));
   if (((uintptr_t)workspace & (kAlign - 1)) != 0) return bad("workspace must be 256-byte aligned");
   const Layout wl = layout((int32_t)B, (int32_t)Q, (int32_t)Hq, (int32_t)Hkv, (int32_t)d, Sp, S);
   if (workspace_bytes < wl.total)
     return fd::record_error(FD_ERR_WORKSPACE_TOO_SMALL, "workspace is smaller than fd_shared_prefix_workspace_size");
-  if (fd::prefix_row_tiles(B, Q * G, group_start ? P : 1, 16) > 65535) return unsupported("grid too large");
+  if (fd::prefix_row_tiles(B, Q * G, group_start != nullptr, P, 16) > 65535) return unsupported("grid too large");
 
   fd::PrefixParams p;
   memset(&p, 0, sizeof p);
@@ -242,9 +259,6 @@ static fd_status run_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix
   p.k_scale = fp8 ? k_scale : nullptr;
   p.v_scale = fp8 ? v_scale : nullptr;
 
-  // ---- the prompt pass: tensor cores for bf16 and FP8, CUDA cores for f32 or when asked for
-  // (with FP8 that is refused with the rows' own keys below)
-  const bool tc = kd != FD_F32 && path != FD_PATH_SIMT;
   CUtensorMap tk, tv;
   if (tc) {
     uint32_t tokens, lines;

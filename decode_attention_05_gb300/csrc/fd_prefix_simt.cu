@@ -218,7 +218,7 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t stream) {
   cudaError_t e = opt_in.apply(kernel, (int)sizeof(Smem<D, BM>));
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.S, (unsigned)p.Hkv,
-                  (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start ? p.P : 1, BM));
+                  (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start != nullptr, p.P, BM));
   return launch_pdl(kernel, grid, kThreads, sizeof(Smem<D, BM>), stream, p);
 }
 

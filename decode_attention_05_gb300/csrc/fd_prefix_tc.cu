@@ -714,7 +714,7 @@ cudaError_t launch(const PrefixParams& p, const CUtensorMap& tk, const CUtensorM
   cudaError_t e = opt_in.apply(kernel, (int)smem_bytes<SH>());
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.S, (unsigned)p.Hkv,
-                  (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start ? p.P : 1, 2 * kRows));
+                  (unsigned)prefix_row_tiles(p.B, (int64_t)p.Q * p.G, p.group_start != nullptr, p.P, 2 * kRows));
   return launch_pdl(kernel, grid, SH::THREADS, smem_bytes<SH>(), stream, tk, tv, p);
 }
 

@@ -578,8 +578,10 @@ FD_API size_t fd_shared_prefix_workspace_size(int32_t B, int32_t Q, int32_t Hq, 
                                               int32_t d, int32_t P, int64_t L_prefix_cap,
                                               int64_t L_cap, int32_t prefix_splits,
                                               int32_t num_splits);
-/* Split count of the prompts that such a call uses: prefix_splits, or for 0 the count that
- * gives one wave of CTAs over (row tile, kv head, split), no split below 256 tokens. */
+/* Split count of the prompts that such a call uses on the tensor cores: prefix_splits, or for 0
+ * the count that gives one wave of CTAs over (row tile, kv head, split), no split below 256
+ * tokens.  (f32 caches, whose pass runs on CUDA cores, take two CTAs per SM and splits of 128
+ * tokens or more.) */
 FD_API int32_t fd_resolve_prefix_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t P,
                                         int64_t L_cap, int32_t prefix_splits);
 

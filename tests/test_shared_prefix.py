@@ -231,6 +231,7 @@ class Case:
 def _run(case, flags=0, **over):
     a = {**case.args(), **over}
     ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    ws[256:].view(torch.float32).fill_(3.0)    # what an earlier call may have left
     out, lse = fd.decode_attention_shared_prefix(workspace=ws, **a)
     assert fd.read_device_error(ws) == flags
     return out, lse
@@ -299,6 +300,16 @@ def test_many_groups():
     groups = tuple(((i * 5) % 3, (i * 37) % 200) for i in range(70))
     c = Case(Hq=4, Hkv=2, groups=groups, own=(3, 0, 17), behind=3, seed=4)
     c.check(*_run(c))
+
+
+@gpu
+@pytest.mark.parametrize("cache", [BF, F8, F32])
+@pytest.mark.parametrize("rows", [1, 3, 64])
+def test_one_group_and_rows_behind_it(cache, rows):
+    c = Case(F32 if cache == F32 else BF, cache, groups=((rows, 150),), own=(5, 33, 1), behind=rows + 1, seed=rows)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    ws[256:].view(torch.float32).fill_(3.0)    # what an earlier call may have left
+    c.check(*fd.decode_attention_shared_prefix(workspace=ws, **c.args()))
 
 
 @gpu
@@ -495,6 +506,26 @@ def test_streams_and_shared_workspace():
     s.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     other.check(*got2)
+
+
+@gpu
+@pytest.mark.parametrize("seed", range(40))
+def test_random_draws(seed):
+    """Random types, heads, groups, lengths, layouts and split counts."""
+    import random
+    r = random.Random(seed)
+    cache = r.choice([BF, BF, F8, F32])
+    Hkv = r.choice([1, 2, 3, 4])
+    G = r.choice([1, 2, 4, 8])
+    Q = r.choice([1, 1, 2, 3]) if G <= 4 else 1
+    groups = tuple((r.choice([0, 1, 2, 7, 40]), r.choice([0, 1, 63, 128, 200, 333, 700]))
+                   for _ in range(r.choice([1, 1, 2, 5])))
+    if sum(n for n, _ in groups) == 0:
+        groups = ((3, 150),)
+    c = Case(F32 if cache == F32 else BF, cache, 128 if cache == F8 else r.choice([64, 128]), Hkv * G, Hkv, Q,
+             groups, [r.choice([0, 1, 5, 33, 120]) for _ in range(6)], page=r.choice([0, 8, 16, 32, 128]),
+             behind=r.choice([0, 0, 2]), cap=704, seed=seed)
+    c.check(*_run(c, prefix_splits=r.choice([0, 0, 1, 3]), num_splits=r.choice([0, 0, 2])))
 
 
 @gpu
