@@ -27,16 +27,23 @@
 // (about 24 bytes a cycle: 2700 cycles) are near balance; several row tiles read a prompt's
 // tiles from L2.
 //
-// Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 the TMA producer, 9 and 10 the issuers.  Tensor
-// memory: S_0, S_1 (128 columns each, P over their first halves), O_0, O_1 (d each).  Shared
+// Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 the TMA producer, 9 and 10 the issuers,
+// 12-19 the widening (FP8).  Tensor memory: S_0, S_1 (128 columns each, P over their first halves), O_0, O_1 (d each).  Shared
 // memory: Q (2 x 128 rows), then a ring of K and V tiles (32 KB at d = 128, 5 of them), each
 // [64-dim slab][token][128 B], 128-byte swizzle.  A page of fewer than 128 tokens is loaded
 // slab by slab, so that a tile has the same layout whatever the page size.
 //
 // FP8 caches: TMA fills a ring of code tiles (16 KB), and two more warpgroups widen them, one
-// the K and one the V tiles, to f16 (exactly: E4M3 fits f16) into the operand ring, so the products are those of f16 q, K, P
-// and V.  (8-bit products would need q and P in 8 bits.)  A kv head's scale of K multiplies
-// the scores, its scale of V the output.
+// the K and one the V tiles, to f16 (exactly: E4M3 fits f16) into the operand ring, so the
+// products are those of f16 q, K, P and V.  (8-bit products would need q and P in 8 bits.)  A
+// weight in f16 is off by 2^-11 of itself or, below 2^-14, by 2^-25: over n keys the output by
+// at most n 2^-25 max |v|, far below its own rounding.  A kv head's scale of K multiplies the
+// scores, its scale of V the output.
+//
+// Measured (GB300; 8 kv heads, d = 128): 64 rows of 64 heads on 131072 tokens, bf16: 172 us of
+// this kernel, 1.6 PFLOP/s on 144 SMs; 512 rows a kv head on 16384 tokens 34 us, 10 us of them
+// the start and the 19 MB of partials; 128 rows of 32 heads on 32768 tokens, FP8: 62 us, bound
+// by shared memory (operands, codes in, tiles widened out).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -225,8 +232,8 @@ __device__ void produce(const PrefixParams& p, const PrefixTile& t, int g, int n
 }
 
 // ---------------------------------------------------------------- widening (FP8, two warpgroups)
-// Warpgroup kv widens the K (0) or V (1) tiles, thread r token row r of each: 16 codes of one 16-byte group become two groups
-// of f16.  A quarter warp's eight rows hit eight different bank groups in both layouts.  Rows
+// Warpgroup kv widens the K (0) or V (1) tiles, thread r token row r of each: 16 codes of one
+// 16-byte group become two groups of f16.  A quarter warp's eight rows hit eight different bank groups in both layouts.  Rows
 // of tokens without weight become zeros.
 template <class SH>
 __device__ void widen(const PrefixParams& p, const PrefixTile& t, int n_tiles, int raw_stages, uint8_t* base,
