@@ -83,6 +83,38 @@ int32_t simt_splits(int32_t B, int32_t Q, int32_t Hq, int32_t Hkv, int32_t P, in
   return prompt_splits(B, Q, Hq, Hkv, P, L_cap, prefix_splits, 64, 2, 128);
 }
 
+// Fewer splits of the tensor-core pass where SMs left to the pass over the rows' own keys,
+// which runs at the same time, shorten the whole: the prompts get SMs in proportion to their
+// work.  Work is in SM microseconds, from sizes alone (own rows taken as half full):
+//   prompts  units x tiles x 0.85 us a 128-token tile (1.2 with two row tiles, 1.6 with pages of
+//            up to 16 tokens, 0.2 more for FP8), times 1.7, the weight that fitted best
+//   own      SMs x (3 us, 6 with more than 16 query rows per kv head, + bytes / 5.8 TB/s)
+// Since the rows may be shorter than their capacity, the prompt pass may get at most 7 us or 12 %
+// longer than on all SMs; and it never gives up SMs that the own pass has no CTAs for.
+// Measured (one wave of splits -> this count): 32 rows on 8192 tokens, own 1024, 16-token pages
+// 36.7 -> 27.9 us (19 -> 8 splits), contiguous 34.7 -> 29.7 (6), 48 rows on 3 prompts 31.5 ->
+// 28.3 (6 -> 3), FP8 48 rows on 10000 tokens 36.9 -> 31.5 (19 -> 9 or 10), 64 rows on 4096 tokens
+// 31.1 -> 25.0 (16 -> 6).
+int32_t side_by_side_splits(const fd::PrefixParams& p, int32_t wave, int d, bool fp8, double own_bytes,
+                            int64_t own_ctas) {
+  const double sms = fd::sm_count();
+  if (sms <= 0) return wave;
+  const int64_t per = ((int64_t)(p.B + p.P - 1) / p.P) * p.Q * p.G;
+  const double units = (double)p.Hkv * std::min(p.P, p.B) * ((per + kRowTile - 1) / kRowTile);
+  const int64_t tiles = (p.L_cap + 127) / 128;
+  double tile_us = per > 128 ? 1.2 : 0.85;
+  if (p.page_size > 0 && p.page_size <= 16) tile_us = 1.6;
+  if (fp8) tile_us += 0.2;
+  if (d == 64) tile_us *= 0.6;
+  const double prompts = units * tiles * tile_us * 1.7;
+  const double own = sms * ((p.Q * p.G > fd::kMaxNarrowRows ? 6.0 : 3.0) + own_bytes / 2 / 5.8e6);
+  const double share = std::max(sms * prompts / (prompts + own), sms - (double)((own_ctas + 1) / 2));
+  int32_t s = (int32_t)std::max<int64_t>(1, std::min<int64_t>(wave, (int64_t)(share / units + 0.5)));
+  auto us = [&](int32_t n) { return (double)((tiles + n - 1) / n) * tile_us; };
+  while (s < wave && us(s) > us(wave) + std::max(7.0, 0.12 * us(wave))) ++s;
+  return s;
+}
+
 struct PromptPass {
   const fd::PrefixParams* p;
   const CUtensorMap *tk, *tv;       // tk nullptr: CUDA cores
@@ -250,6 +282,8 @@ static fd_status run_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix
   p.page_size = prefix_table ? page_size : 0;
   p.log2_page = log2_page;
   p.S = Sp;
+  if (tc && prefix_splits == 0)
+    p.S = side_by_side_splits(p, Sp, (int)d, fp8, 2.0 * B * L_cap * Hkv * d * es, B * Hkv * S);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.lse_part = reinterpret_cast<float*>(ws + wl.lse_off);
   p.o_part = reinterpret_cast<float*>(ws + wl.o_off);
@@ -282,7 +316,7 @@ static fd_status run_shared_prefix(const fd_tensor* q, const fd_tensor* k_prefix
   memset(&mp, 0, sizeof mp);
   mp.rows = (int32_t)(B * Q * Hq);
   mp.Q = (int32_t)Q, mp.Hq = (int32_t)Hq, mp.d = (int32_t)d;
-  mp.S[0] = Sp, mp.S[1] = S;
+  mp.S[0] = p.S, mp.S[1] = S;
   mp.lse[0] = p.lse_part, mp.o[0] = p.o_part;
   float *lse_own = nullptr, *o_own = nullptr;
   fd_workspace_partials(workspace, (int32_t)B, (int32_t)(Q * Hq), (int32_t)d, S, &lse_own, &o_own);

@@ -540,7 +540,8 @@ FD_API fd_status fd_append_kv(const fd_tensor* q, const fd_tensor* k, const fd_t
  *                block_table.
  *   page_size    of whichever of prefix_table and block_table is given; 0 if neither is.
  *   prefix_splits  splits of each prompt (even shares of its own length); 0: the count
- *                fd_resolve_prefix_splits reports.
+ *                fd_resolve_prefix_splits reports, or fewer where SMs left to the rows' own keys,
+ *                which are read at the same time, shorten the step (chosen from the sizes).
  *   workspace    fd_shared_prefix_workspace_size bytes, otherwise as fd_decode_attention.
  * With Q query tokens per row every one of them sees the whole prompt, and query j the own
  * keys t <= L_b - Q + j.  A row without any key gets out = 0, lse_out = -infinity.
